@@ -60,6 +60,7 @@ const char* hata_status_string(hata_status_t s) {
     case HATA_ERR_CUDA: return "CUDA error";
     case HATA_ERR_TIMEOUT: return "device-side wait timed out";
     case HATA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
+    case HATA_ERR_NO_PAGES: return "too few free pages in the pool";
   }
   return "unknown status";
 }

@@ -51,6 +51,45 @@ struct PagedCache {
 cudaError_t launch_append_kv(const hata_dims_t& d, const void* new_k, const void* new_v, void* K, void* V,
                              const int32_t* seq_lens, const PagedCache* pg, cudaStream_t stream);
 
+// Norms, position rotation and cache append (hata_rope.cu).
+struct RopeArgs {
+  const void *q_in, *k_in, *v_in;
+  long long q_stride, k_stride, v_stride;
+  const float *q_weight, *k_weight, *table;
+  const int32_t *n_new, *positions, *seq_lens;
+  void *q_out, *K, *V;
+  float eps;
+  int n_tok, n_pos, rot, interleaved;
+};
+cudaError_t launch_norm_rope(const hata_dims_t& d, const RopeArgs& a, const PagedCache* pg, uint32_t* status,
+                             cudaStream_t stream);
+cudaError_t launch_rope_table(float* table, int n_pos, int rot, double theta, cudaStream_t stream);
+
+// Window decode (window > 0, n_tok = 1) and tree attention (window = 0) (hata_span.cu).
+struct SpanArgs {
+  const void *q, *K, *V;
+  const int32_t *seq_lens, *n_new;
+  const uint32_t* mask;
+  void* out;
+  float scale;
+  int n_tok, window, sink;
+};
+constexpr int kMaxTreeTokens = 128;  // new tokens per sequence of one call
+size_t span_ws_bytes(const hata_dims_t& d, int n_tok);
+cudaError_t launch_span(const hata_dims_t& d, const SpanArgs& a, const PagedCache* pg, char* ws, cudaStream_t stream);
+
+// Page bookkeeping and row compaction (hata_pages.cu).
+constexpr int kMaxPageRows = 1024;  // sequences of one call
+size_t pages_ws_bytes(int batch);
+cudaError_t launch_pages_fork(const hata_dims_t& d, const int32_t* parent, int32_t* table, int max_blocks,
+                              int n_blocks, int32_t* seq_lens, int32_t* ref, uint32_t* status, cudaStream_t stream);
+cudaError_t launch_pages_resize(const hata_dims_t& d, const int32_t* new_lens, void* K, void* V, void* codes,
+                                const PagedCache& pg, int32_t* table, int32_t* seq_lens, int32_t* ref, char* ws,
+                                cudaStream_t stream);
+cudaError_t launch_compact(const hata_dims_t& d, int n_tok, const int32_t* keep, const int32_t* n_keep,
+                           const int32_t* n_new, const int32_t* seq_lens, void* K, void* V, void* codes,
+                           const PagedCache* pg, int32_t* new_lens, uint32_t* status, cudaStream_t stream);
+
 // Wk: separate key encoder, or equal to W (one encoder for queries and keys).
 // pg: paged cache, or null for [B][Hkv][max_seq][...] slabs.
 cudaError_t launch_fused_step(const hata_dims_t& d, const WsLayout& L, const void* q, const void* K,

@@ -1,0 +1,405 @@
+// Bookkeeping of a paged cache on the device, so that a whole serving step (roll back, fork, grow,
+// append, attend, accept) is enqueued without a host round trip and can be captured in a graph:
+//   fork     row b takes the pages of row parent[b], all rows read before any is written
+//   resize   every row to its new length: pages past the end freed, a shared partial last page copied
+//            (copy on write) before the row may append to it, new pages allocated
+//   compact  accepted rows of the newest tokens moved to the front of them (K, V and codes)
+// A page is free when its reference count is zero, and the j-th page needed is the j-th lowest free page, so
+// there is no list of free pages to keep, and the result does not depend on the order of threads.
+//
+// Bound: latency.  The tables and counts are a few hundred KB, read and written once; resize's
+// decisions are one CTA (a prefix sum over rows and two passes over the counts), its copies and
+// compact's moves spread over all SMs as 16-byte vectors.
+#include <algorithm>
+
+#include "hata_kernels.cuh"
+
+namespace hata {
+
+namespace {
+
+constexpr int kPgThreads = 1024;
+constexpr int kPgWarps = kPgThreads / 32;
+constexpr int kForkCols = 8;  // table columns of one fork CTA
+
+// ---- fork: a CTA owns 8 columns of the table: it reads them for every row, then writes them
+__global__ void __launch_bounds__(256)
+    pages_fork_kernel(const int32_t* __restrict__ parent, int32_t* table, int32_t* seq_lens, int32_t* ref, int B,
+                      int max_blocks, int n_blocks, uint32_t* status) {
+  extern __shared__ int32_t fork_old[];  // [B][kForkCols], then for CTA 0 the lengths [B]
+  const int c0 = (int)blockIdx.x * kForkCols, tid = threadIdx.x;
+  for (int e = tid; e < B * kForkCols; e += blockDim.x) {
+    const int c = c0 + e % kForkCols;
+    fork_old[e] = c < max_blocks ? table[(size_t)(e / kForkCols) * max_blocks + c] : -1;
+  }
+  int32_t* lens = fork_old + (size_t)B * kForkCols;
+  if (blockIdx.x == 0)
+    for (int b = tid; b < B; b += blockDim.x) lens[b] = seq_lens[b];
+  __syncthreads();
+  for (int e = tid; e < B * kForkCols; e += blockDim.x) {
+    const int b = e / kForkCols, c = c0 + e % kForkCols, pa = parent[b];
+    if (pa < 0 || pa >= B || pa == b) continue;
+    const int was = fork_old[e], now = fork_old[pa * kForkCols + e % kForkCols];
+    if (c >= max_blocks || was == now) continue;  // the same page (or none) on both sides
+    if (was >= 0 && was < n_blocks) atomicSub(&ref[was], 1);
+    if (now >= 0 && now < n_blocks) atomicAdd(&ref[now], 1);
+    table[(size_t)b * max_blocks + c] = now;
+  }
+  if (blockIdx.x == 0)
+    for (int b = tid; b < B; b += blockDim.x) {
+      const int pa = parent[b];
+      if (pa >= B) set_status(status, HATA_ERR_INVALID_ARG);
+      if (pa >= 0 && pa < B && pa != b) seq_lens[b] = lens[pa];
+    }
+}
+
+// ---- resize: the decisions, by one CTA
+struct ResizeParams {
+  const int32_t* new_lens;
+  int32_t *table, *seq_lens, *ref;
+  int32_t* copies;  // workspace: per row (source page, target page, rows), source -1: nothing to copy
+  int B, max_seq, max_blocks, n_blocks, block_shift;
+  uint32_t* status;
+};
+
+__global__ void __launch_bounds__(kPgThreads) pages_resize_kernel(const ResizeParams p) {
+  extern __shared__ int32_t rs_smem[];
+  int32_t* s_old = rs_smem;            // length before
+  int32_t* s_tail = s_old + p.B;       // page a growing row would write into, else -1
+  int32_t* s_first = s_tail + p.B;     // first column that gets a page
+  int32_t* s_pre = s_first + p.B;      // pages needed by earlier rows; [B]: by all
+  __shared__ int32_t warp_sum[kPgWarps];
+  __shared__ int32_t s_total;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.B;
+  const int bs = 1 << p.block_shift;
+  auto pages_of = [&](int len) { return (int)(((long long)len + bs - 1) >> p.block_shift); };
+  // a row whose old or new length lies outside [0, max_seq] stays as it is
+  auto target = [&](int b, int old) {
+    const int nw = p.new_lens[b];
+    return (nw < 0 || nw > p.max_seq) ? old : nw;
+  };
+  for (int b = tid; b < B; b += kPgThreads) {
+    const int old = p.seq_lens[b], nw = p.new_lens[b];
+    const bool ok = old >= 0 && old <= p.max_seq;
+    if (!ok || nw < 0 || nw > p.max_seq) set_status(p.status, HATA_ERR_INVALID_ARG);
+    s_old[b] = ok ? old : -1;
+    s_tail[b] = -1;
+    p.copies[3 * b] = -1;
+  }
+  __syncthreads();
+  // frees: a warp per row
+  for (int b = warp; b < B; b += kPgWarps) {
+    const int old = s_old[b];
+    if (old < 0) continue;
+    const int n_new = pages_of(target(b, old)), n_old = pages_of(old);
+    for (int c = n_new + lane; c < n_old; c += 32) {
+      int32_t* e = &p.table[(size_t)b * p.max_blocks + c];
+      const int page = *e;
+      *e = -1;
+      if (page < 0 || page >= p.n_blocks) {
+        set_status(p.status, HATA_ERR_INVALID_ARG);
+      } else if (atomicSub(&p.ref[page], 1) <= 0) {  // counted less often than it is used
+        atomicAdd(&p.ref[page], 1);
+        set_status(p.status, HATA_ERR_INVALID_ARG);
+      }
+    }
+  }
+  __syncthreads();
+  // growing rows whose last page is partly filled and shared
+  for (int b = tid; b < B; b += kPgThreads) {
+    const int old = s_old[b];
+    if (old < 0 || target(b, old) <= old || !(old & (bs - 1))) continue;
+    const int page = p.table[(size_t)b * p.max_blocks + pages_of(old) - 1];
+    if (page >= 0 && page < p.n_blocks) s_tail[b] = page;
+    else set_status(p.status, HATA_ERR_INVALID_ARG);
+  }
+  __syncthreads();
+  // needs: of the rows that share a tail page and grow, the earlier ones copy it and, when nobody else holds
+  // it, the last one keeps it (what rows handled one after another would do)
+  for (int b = tid; b < B; b += kPgThreads) {
+    const int old = s_old[b];
+    int need = 0, first = 0;
+    if (old >= 0) {
+      const int nw = target(b, old), n_old = pages_of(old);
+      int copy = 0;
+      if (nw > old) {
+        if (s_tail[b] >= 0) {
+          const int held = __ldcg(&p.ref[s_tail[b]]);
+          if (held > 1) {
+            int before = 0;
+            for (int o = 0; o < b; ++o) before += s_tail[o] == s_tail[b];
+            copy = held - before > 1;
+          }
+        }
+        need = pages_of(nw) - n_old + copy;
+      }
+      first = n_old - copy;
+    }
+    s_first[b] = first;
+    s_pre[b] = need;
+  }
+  __syncthreads();
+  // exclusive prefix over rows
+  int carry = 0;
+  for (int b0 = 0; b0 < B; b0 += kPgThreads) {
+    const int v = b0 + tid < B ? s_pre[b0 + tid] : 0;
+    int tot = 0;
+    const int x = block_exclusive_scan<kPgThreads>(v, warp_sum, &tot);
+    if (b0 + tid < B) s_pre[b0 + tid] = carry + x;
+    carry += tot;
+  }
+  if (tid == 0) s_pre[B] = carry;
+  const int total = carry;
+  // free pages: each warp counts its share of the pages, then hands out the free ones of its share
+  const int per = ((p.n_blocks + kPgWarps - 1) / kPgWarps + 31) / 32 * 32;
+  const int p0 = min(p.n_blocks, warp * per), p1 = min(p.n_blocks, p0 + per);
+  int mine = 0;
+  if (total > 0) {
+#pragma unroll 8
+    for (int q = p0 + lane; q < p1; q += 32) mine += __ldcg(&p.ref[q]) == 0;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) warp_sum[warp] = mine;
+  __syncthreads();
+  if (warp == 0) {
+    int x = warp_sum[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_total = x;
+    warp_sum[lane] = x;
+  }
+  __syncthreads();
+  const bool enough = s_total >= total;
+  if (!enough && tid == 0) set_status(p.status, HATA_ERR_NO_PAGES);
+  if (enough && total > 0) {
+    int rank = warp_sum[warp] - mine;  // free pages before this warp's share
+    for (int q0 = p0; q0 < p1 && rank < total; q0 += 32) {
+      const int q = q0 + lane;
+      const bool is_free = q < p1 && __ldcg(&p.ref[q]) == 0;
+      const unsigned m = __ballot_sync(0xffffffffu, is_free);
+      const int r = rank + __popc(m & ((1u << lane) - 1u));
+      if (is_free && r < total) {
+        int lo = 0, hi = B;  // the row b with s_pre[b] <= r < s_pre[b + 1]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (s_pre[mid] <= r) lo = mid;
+          else hi = mid;
+        }
+        p.table[(size_t)lo * p.max_blocks + s_first[lo] + (r - s_pre[lo])] = q;
+        p.ref[q] = 1;
+      }
+      rank += __popc(m);
+    }
+  }
+  __syncthreads();
+  for (int b = tid; b < B; b += kPgThreads) {
+    const int old = s_old[b];
+    if (old < 0) continue;
+    const int nw = target(b, old), n_old = pages_of(old);
+    if (nw > old) {
+      if (!enough) continue;  // no row grows
+      if (s_first[b] < n_old) {
+        p.copies[3 * b + 1] = p.table[(size_t)b * p.max_blocks + n_old - 1];
+        p.copies[3 * b + 2] = old & (bs - 1);
+        p.copies[3 * b] = s_tail[b];
+        atomicSub(&p.ref[s_tail[b]], 1);
+      }
+    }
+    p.seq_lens[b] = nw;
+  }
+}
+
+// ---- copies: one CTA per (row, KV head, piece) and tensor; a page's rows of one head are contiguous
+__global__ void __launch_bounds__(256)
+    pages_copy_kernel(const int32_t* __restrict__ copies, unsigned char* K, unsigned char* V, unsigned char* codes,
+                      int hkv, int bs, int row_bytes, int code_bytes, int n_piece) {
+  const int b = blockIdx.y;
+  const int src = copies[3 * b];
+  if (src < 0) return;
+  const int dst = copies[3 * b + 1], rows = copies[3 * b + 2];
+  int x = (int)blockIdx.x;
+  const int piece = x % n_piece;
+  x /= n_piece;
+  const int g = x % hkv, t = x / hkv;
+  unsigned char* base = t == 0 ? K : t == 1 ? V : codes;
+  const int rb = t < 2 ? row_bytes : code_bytes;
+  unsigned char* from = base + ((size_t)src * hkv + g) * bs * rb;
+  unsigned char* to = base + ((size_t)dst * hkv + g) * bs * rb;
+  const size_t bytes = (size_t)rows * rb, nv = bytes / 16;
+  for (size_t e = (size_t)piece * 256 + threadIdx.x; e < nv; e += (size_t)n_piece * 256)
+    reinterpret_cast<uint4*>(to)[e] = reinterpret_cast<const uint4*>(from)[e];
+  if (piece == 0) {  // the last bytes of narrow codes
+    const size_t e = nv * 16 + 2 * threadIdx.x;
+    if (e < bytes) *reinterpret_cast<uint16_t*>(to + e) = *reinterpret_cast<const uint16_t*>(from + e);
+  }
+}
+
+// ---- compact: row base + keep[j] to row base + j, j < n_keep, keep ascending.  A target row j is never the
+// source of a later chunk (source j' >= j'), so a CTA that owns a column slice of (b, head, tensor) loads a
+// chunk of rows, waits for all of it, stores it and goes on.
+struct CompactParams {
+  const int32_t *keep, *n_keep, *n_new, *seq_lens;
+  unsigned char *K, *V, *codes;
+  int32_t* new_lens;
+  const int32_t* block_table;
+  uint32_t* status;
+  int B, n_tok, Hkv, max_seq, row_bytes, code_bytes;
+  int block_shift, n_blocks, max_blocks;
+};
+
+constexpr int kCpThreads = 256;
+constexpr int kCpBatch = 4;  // pieces a thread holds between load and store
+
+template <typename E, bool PAGED>
+__device__ __forceinline__ void compact_rows(const CompactParams& p, E* base, int per_row, int b, int g, int start,
+                                             int n_keep) {
+  // pieces of type E: `per_row` of them make a row, and consecutive threads take consecutive pieces
+  const int32_t* keep = p.keep + (size_t)b * p.n_tok;
+  auto row_of = [&](int t, bool& ok) -> size_t {
+    if constexpr (PAGED) {
+      const int blk = p.block_table[(size_t)b * p.max_blocks + (t >> p.block_shift)];
+      if (blk < 0 || blk >= p.n_blocks) {
+        ok = false;
+        return 0;
+      }
+      return (((size_t)blk * p.Hkv + g) << p.block_shift) + (size_t)(t & ((1 << p.block_shift) - 1));
+    } else {
+      return ((size_t)b * p.Hkv + g) * p.max_seq + t;
+    }
+  };
+  const long long n = (long long)n_keep * per_row;
+  for (long long e0 = 0; e0 < n; e0 += kCpThreads * kCpBatch) {
+    E v[kCpBatch];
+    size_t to[kCpBatch];
+    bool moves[kCpBatch];
+#pragma unroll
+    for (int u = 0; u < kCpBatch; ++u) {
+      const long long e = e0 + u * kCpThreads + threadIdx.x;
+      moves[u] = false;
+      if (e >= n) continue;
+      const int j = (int)(e / per_row), c = (int)(e % per_row);
+      const int k = keep[j];
+      if (k == j) continue;
+      bool ok = true;
+      const size_t from = row_of(start + k, ok);
+      const size_t dst = row_of(start + j, ok);
+      if (!ok) {
+        set_status(p.status, HATA_ERR_INVALID_ARG);
+        continue;
+      }
+      moves[u] = true;
+      to[u] = dst * per_row + c;
+      v[u] = base[from * per_row + c];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kCpBatch; ++u)
+      if (moves[u]) base[to[u]] = v[u];
+    __syncthreads();
+  }
+}
+
+template <bool PAGED>
+__global__ void __launch_bounds__(kCpThreads) compact_kernel(const CompactParams p) {
+  const int b = blockIdx.y, g = (int)blockIdx.x % p.Hkv, t = (int)blockIdx.x / p.Hkv, tid = threadIdx.x;
+  const int L = p.seq_lens[b], n_b = p.n_new ? p.n_new[b] : p.n_tok, n_keep = p.n_keep[b];
+  bool bad = n_b < 0 || n_b > p.n_tok || L < n_b || L > p.max_seq || n_keep < 0 || n_keep > n_b;
+  if (!bad) {
+    const int32_t* keep = p.keep + (size_t)b * p.n_tok;
+    int wrong = 0;
+    for (int j = tid; j < n_keep; j += kCpThreads) {
+      const int k = keep[j];
+      wrong |= k < 0 || k >= n_b || (j > 0 && keep[j - 1] >= k);
+    }
+    bad = __syncthreads_or(wrong) != 0;
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    if (bad) set_status(p.status, HATA_ERR_INVALID_ARG);
+    if (p.new_lens) p.new_lens[b] = bad ? L : L - n_b + n_keep;
+  }
+  if (bad) return;
+  if (t < 2) {
+    compact_rows<uint4, PAGED>(p, reinterpret_cast<uint4*>(t == 0 ? p.K : p.V), p.row_bytes / 16, b, g, L - n_b, n_keep);
+  } else if (p.code_bytes == 2) {
+    compact_rows<uint16_t, PAGED>(p, reinterpret_cast<uint16_t*>(p.codes), 1, b, g, L - n_b, n_keep);
+  } else {
+    compact_rows<uint32_t, PAGED>(p, reinterpret_cast<uint32_t*>(p.codes), p.code_bytes / 4, b, g, L - n_b, n_keep);
+  }
+}
+
+}  // namespace
+
+size_t pages_ws_bytes(int batch) { return align_up(kStatusBytes, 16) + align_up((size_t)batch * 12, 16); }
+
+cudaError_t launch_pages_fork(const hata_dims_t& d, const int32_t* parent, int32_t* table, int max_blocks,
+                              int n_blocks, int32_t* seq_lens, int32_t* ref, uint32_t* status, cudaStream_t st) {
+  const unsigned grid = (unsigned)((max_blocks + kForkCols - 1) / kForkCols);
+  const size_t smem = (size_t)d.batch * (kForkCols + 1) * 4;  // at most 36 KB: d.batch <= kMaxPageRows
+  pages_fork_kernel<<<grid, 256, smem, st>>>(parent, table, seq_lens, ref, d.batch, max_blocks, n_blocks, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pages_resize(const hata_dims_t& d, const int32_t* new_lens, void* K, void* V, void* codes,
+                                const PagedCache& pg, int32_t* table, int32_t* seq_lens, int32_t* ref, char* ws,
+                                cudaStream_t st) {
+  ResizeParams p;
+  p.new_lens = new_lens;
+  p.table = table;
+  p.seq_lens = seq_lens;
+  p.ref = ref;
+  p.copies = reinterpret_cast<int32_t*>(ws + kStatusBytes);
+  p.B = d.batch;
+  p.max_seq = d.max_seq;
+  p.max_blocks = pg.max_blocks;
+  p.n_blocks = pg.n_blocks;
+  p.block_shift = pg.block_shift;
+  p.status = reinterpret_cast<uint32_t*>(ws);
+  pages_resize_kernel<<<1, kPgThreads, (size_t)(4 * d.batch + 1) * 4, st>>>(p);  // at most 16 KB
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int bs = 1 << pg.block_shift, row_bytes = kHeadDim * (d.dtype == HATA_BF16 ? 2 : 4);
+  const int n_piece = std::max(1, std::min(64, bs / 64));  // 16-32 KB of a K page per CTA
+  const int tensors = codes ? 3 : 2;
+  pages_copy_kernel<<<dim3((unsigned)(tensors * d.n_kv_heads * n_piece), (unsigned)d.batch), 256, 0, st>>>(
+      p.copies, static_cast<unsigned char*>(K), static_cast<unsigned char*>(V), static_cast<unsigned char*>(codes),
+      d.n_kv_heads, bs, row_bytes, d.hash_bits / 8, n_piece);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_compact(const hata_dims_t& d, int n_tok, const int32_t* keep, const int32_t* n_keep,
+                           const int32_t* n_new, const int32_t* seq_lens, void* K, void* V, void* codes,
+                           const PagedCache* pg, int32_t* new_lens, uint32_t* status, cudaStream_t st) {
+  CompactParams p{};
+  p.keep = keep;
+  p.n_keep = n_keep;
+  p.n_new = n_new;
+  p.seq_lens = seq_lens;
+  p.K = static_cast<unsigned char*>(K);
+  p.V = static_cast<unsigned char*>(V);
+  p.codes = static_cast<unsigned char*>(codes);
+  p.new_lens = new_lens;
+  p.status = status;
+  p.B = d.batch;
+  p.n_tok = n_tok;
+  p.Hkv = d.n_kv_heads;
+  p.max_seq = d.max_seq;
+  p.row_bytes = kHeadDim * (d.dtype == HATA_BF16 ? 2 : 4);
+  p.code_bytes = d.hash_bits / 8;
+  if (pg) {
+    p.block_table = pg->block_table;
+    p.block_shift = pg->block_shift;
+    p.n_blocks = pg->n_blocks;
+    p.max_blocks = pg->max_blocks;
+  }
+  if (d.batch > 65535) return cudaErrorNotSupported;
+  const dim3 grid((unsigned)(d.n_kv_heads * (codes ? 3 : 2)), (unsigned)d.batch);
+  if (pg) compact_kernel<true><<<grid, kCpThreads, 0, st>>>(p);
+  else compact_kernel<false><<<grid, kCpThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace hata

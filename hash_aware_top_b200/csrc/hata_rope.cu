@@ -1,0 +1,287 @@
+// Norms of queries and keys for each head, the position rotation and the cache append in one
+// pass over a projection's output: the step between the projection and hata_decode_step (which
+// encodes and scores the new key from its cache slot).
+//
+// For token i of sequence b, with slot s = L_b - n_b + i and position t = positions[b][i] (or s):
+//   y = x * rsqrt(mean(x^2) + eps) * w          (fp32; w NULL: y = x)
+//   (y_a, y_b) -> (y_a c - y_b s', y_b c + y_a s')   with (c, s') = table[t][.][pair]
+// for the rot / 2 pairs of the first rot elements: (e, e + rot / 2) or, interleaved, (2 e, 2 e + 1).
+// Queries go to q_out[b][h][i], keys to K[.][g][s], values are copied to V[.][g][s].  Everything
+// is fp32 between the load and the one rounding of the store.
+//
+// Bound by memory: each row is read once and written once.  A row is 16 (bf16) or 32 (fp32) lanes
+// of 16 bytes, so the mean square is a shuffle tree and the partner of a half-split pair lies rot / 2
+// elements, a whole number of lanes, away.  The 8 warps of a CTA take 8 consecutive tokens and the same rows of
+// each, so that the scattered stores of neighbouring tokens meet in L2 as 2 KB runs per head.
+#include "hata_kernels.cuh"
+
+namespace hata {
+
+namespace {
+
+constexpr int kRopeWarps = 8;
+constexpr int kRopeBatch = 4;  // row steps whose loads are in flight together
+
+struct RopeParams {
+  const void *q_in, *k_in, *v_in;
+  long long q_stride, k_stride, v_stride;  // elements between tokens
+  const float *q_weight, *k_weight;
+  const float* table;
+  const int32_t *n_new, *positions, *seq_lens;
+  void *q_out, *K, *V;
+  const int32_t* block_table;
+  uint32_t* status;
+  float eps;
+  int n_tok, Hq, Hkv, max_seq, n_pos, rot;
+  int block_shift, n_blocks, max_blocks;
+  int tok_blocks;      // ceil(n_tok / kRopeWarps)
+  int steps_per_warp;  // row steps of one warp
+  int n_split;         // warps that share a token's rows
+};
+
+template <typename T>
+struct Vec16 {
+  static constexpr int N = 16 / sizeof(T);
+  static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[N]);
+  static __device__ __forceinline__ uint4 pack(const float (&x)[N]);
+};
+template <>
+__device__ __forceinline__ void Vec16<float>::unpack(const uint4& u, float (&x)[4]) {
+  x[0] = __uint_as_float(u.x);
+  x[1] = __uint_as_float(u.y);
+  x[2] = __uint_as_float(u.z);
+  x[3] = __uint_as_float(u.w);
+}
+template <>
+__device__ __forceinline__ uint4 Vec16<float>::pack(const float (&x)[4]) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+template <>
+__device__ __forceinline__ void Vec16<__nv_bfloat16>::unpack(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // a bf16 is the high half of the fp32 of the same value
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+template <>
+__device__ __forceinline__ uint4 Vec16<__nv_bfloat16>::pack(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T, bool INTER, bool PAGED>
+__global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeParams p) {
+  constexpr int N = Vec16<T>::N;           // elements of a lane's vector
+  constexpr int LANES = kHeadDim / N;      // lanes of a row
+  constexpr int RPS = 32 / LANES;          // rows of one warp step
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int li = lane % LANES, sub = lane / LANES;
+  const int b = (int)(blockIdx.y), tb = (int)(blockIdx.x) / p.n_split, sp = (int)(blockIdx.x) % p.n_split;
+  const int i = tb * kRopeWarps + warp;
+  const int n_b = p.n_new ? p.n_new[b] : p.n_tok;
+  const int L = p.seq_lens[b];
+  if (n_b < 0 || n_b > p.n_tok || L < n_b || L > p.max_seq) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) set_status(p.status, HATA_ERR_INVALID_ARG);
+    return;
+  }
+  if (i >= n_b) return;
+  const int slot = L - n_b + i;
+  const size_t tok = (size_t)b * p.n_tok + i;
+  const int pos = p.positions ? p.positions[tok] : slot;
+  if (p.rot > 0 && (pos < 0 || pos >= p.n_pos)) {
+    if (lane == 0) set_status(p.status, HATA_ERR_INVALID_ARG);
+    return;
+  }
+  // the cache row of KV head 0; head g is `head_rows` * g rows on
+  size_t row0, head_rows;
+  bool stored = true;
+  if constexpr (PAGED) {
+    const int blk = p.block_table[(size_t)b * p.max_blocks + (slot >> p.block_shift)];
+    stored = blk >= 0 && blk < p.n_blocks;
+    if (!stored && lane == 0) set_status(p.status, HATA_ERR_INVALID_ARG);
+    head_rows = (size_t)1 << p.block_shift;
+    row0 = (((size_t)(stored ? blk : 0) * p.Hkv) << p.block_shift) + (size_t)(slot & ((1 << p.block_shift) - 1));
+  } else {
+    head_rows = (size_t)p.max_seq;
+    row0 = (size_t)b * p.Hkv * p.max_seq + slot;
+  }
+  const int half = p.rot / 2, e0 = li * N;
+  // this lane's cosines and sines (half-split: one pair per element; interleaved: one per two)
+  float c[N], sn[N];
+  int partner = lane;
+  const bool turns = e0 < p.rot;
+  float side = 0.f;  // half-split: -1 for the first element of a pair, +1 for the second
+  if (turns) {
+    const float* row = p.table + (size_t)pos * p.rot;
+    const int f0 = INTER ? e0 / 2 : (e0 < half ? e0 : e0 - half);
+    constexpr int NF = INTER ? N / 2 : N;
+#pragma unroll
+    for (int k = 0; k < NF; ++k) {
+      c[k] = __ldg(row + f0 + k);
+      sn[k] = __ldg(row + half + f0 + k);
+    }
+    if (!INTER) {
+      partner = e0 < half ? lane + half / N : lane - half / N;
+      side = e0 < half ? -1.f : 1.f;
+    }
+  }
+  float wq[N], wk[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    wq[k] = p.q_weight ? __ldg(p.q_weight + e0 + k) : 1.f;
+    wk[k] = p.k_weight ? __ldg(p.k_weight + e0 + k) : 1.f;
+  }
+  const int rows = p.Hq + 2 * p.Hkv;  // query heads, key heads, value heads
+  const T* q = static_cast<const T*>(p.q_in) + tok * (size_t)p.q_stride + e0;
+  const T* kk = static_cast<const T*>(p.k_in) + tok * (size_t)p.k_stride + e0;
+  const T* v = static_cast<const T*>(p.v_in) + tok * (size_t)p.v_stride + e0;
+  const int first = sp * p.steps_per_warp * RPS;
+  const int last = min(rows, first + p.steps_per_warp * RPS);
+  for (int r0 = first; r0 < last; r0 += kRopeBatch * RPS) {
+    uint4 in[kRopeBatch];
+#pragma unroll
+    for (int u = 0; u < kRopeBatch; ++u) {
+      const int r = r0 + u * RPS + sub;
+      if (r < last) {
+        const T* src = r < p.Hq ? q + (size_t)r * kHeadDim
+                                : r < p.Hq + p.Hkv ? kk + (size_t)(r - p.Hq) * kHeadDim
+                                                   : v + (size_t)(r - p.Hq - p.Hkv) * kHeadDim;
+        in[u] = __ldg(reinterpret_cast<const uint4*>(src));
+      } else {
+        in[u] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRopeBatch; ++u) {
+      const int r = r0 + u * RPS + sub;
+      const bool is_q = r < p.Hq, is_v = r >= p.Hq + p.Hkv;
+      float x[N];
+      Vec16<T>::unpack(in[u], x);
+      float ss = 0.f;
+#pragma unroll
+      for (int k = 0; k < N; ++k) ss = fmaf(x[k], x[k], ss);
+#pragma unroll
+      for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const bool normed = is_q ? p.q_weight != nullptr : p.k_weight != nullptr;
+      const float rs = normed ? rsqrtf(ss * (1.f / kHeadDim) + p.eps) : 1.f;
+#pragma unroll
+      for (int k = 0; k < N; ++k) x[k] = x[k] * rs * (is_q ? wq[k] : wk[k]);
+      if (INTER) {
+        if (turns) {
+#pragma unroll
+          for (int k = 0; k < N / 2; ++k) {
+            const float a = x[2 * k], d = x[2 * k + 1];
+            x[2 * k] = a * c[k] - d * sn[k];
+            x[2 * k + 1] = d * c[k] + a * sn[k];
+          }
+        }
+      } else if (p.rot > 0) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const float other = __shfl_sync(0xffffffffu, x[k], partner);
+          if (turns) x[k] = x[k] * c[k] + side * (other * sn[k]);
+        }
+      }
+      if (r >= last) continue;
+      const uint4 o = is_v ? in[u] : Vec16<T>::pack(x);
+      if (is_q) {
+        T* dst = static_cast<T*>(p.q_out) + (((size_t)b * p.Hq + r) * p.n_tok + i) * kHeadDim + e0;
+        *reinterpret_cast<uint4*>(dst) = o;
+      } else if (stored) {
+        const int g = is_v ? r - p.Hq - p.Hkv : r - p.Hq;
+        T* dst = static_cast<T*>(is_v ? p.V : p.K) + (row0 + (size_t)g * head_rows) * kHeadDim + e0;
+        *reinterpret_cast<uint4*>(dst) = o;
+      }
+    }
+  }
+}
+
+template <typename T, bool INTER>
+void launch_rope_t(const RopeParams& prm, bool paged, dim3 grid, cudaStream_t st) {
+  if (paged)
+    norm_rope_kernel<T, INTER, true><<<grid, kRopeWarps * 32, 0, st>>>(prm);
+  else
+    norm_rope_kernel<T, INTER, false><<<grid, kRopeWarps * 32, 0, st>>>(prm);
+}
+
+// table[t][0][i] = cos(t * theta^(-2 i / rot)), table[t][1][i] = sin(..), the angle in fp64: at
+// t = 131072 an fp32 angle would be off by up to 2^-8 radians.
+__global__ void rope_table_kernel(float* __restrict__ table, int n_pos, int half, double theta) {
+  const long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (e >= (long long)n_pos * half) return;
+  const int i = (int)(e % half);
+  const long long t = e / half;
+  const double angle = (double)t * pow(theta, -(double)i / (double)half);
+  double s, c;
+  sincos(angle, &s, &c);
+  table[t * 2 * half + i] = (float)c;
+  table[t * 2 * half + half + i] = (float)s;
+}
+
+}  // namespace
+
+cudaError_t launch_rope_table(float* table, int n_pos, int rot, double theta, cudaStream_t st) {
+  const long long n = (long long)n_pos * (rot / 2), blocks = (n + 255) / 256;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  rope_table_kernel<<<(unsigned)blocks, 256, 0, st>>>(table, n_pos, rot / 2, theta);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_norm_rope(const hata_dims_t& d, const RopeArgs& a, const PagedCache* pg, uint32_t* status,
+                             cudaStream_t st) {
+  RopeParams p{};
+  p.q_in = a.q_in;
+  p.k_in = a.k_in;
+  p.v_in = a.v_in;
+  p.q_stride = a.q_stride;
+  p.k_stride = a.k_stride;
+  p.v_stride = a.v_stride;
+  p.q_weight = a.q_weight;
+  p.k_weight = a.k_weight;
+  p.table = a.table;
+  p.n_new = a.n_new;
+  p.positions = a.positions;
+  p.seq_lens = a.seq_lens;
+  p.q_out = a.q_out;
+  p.K = a.K;
+  p.V = a.V;
+  p.status = status;
+  p.eps = a.eps;
+  p.n_tok = a.n_tok;
+  p.Hq = d.n_q_heads;
+  p.Hkv = d.n_kv_heads;
+  p.max_seq = d.max_seq;
+  p.n_pos = a.n_pos;
+  p.rot = a.rot;
+  if (pg) {
+    p.block_table = pg->block_table;
+    p.block_shift = pg->block_shift;
+    p.n_blocks = pg->n_blocks;
+    p.max_blocks = pg->max_blocks;
+  }
+  const int rps = d.dtype == HATA_BF16 ? 2 : 1;
+  const int steps = (p.Hq + 2 * p.Hkv + rps - 1) / rps;
+  p.tok_blocks = (p.n_tok + kRopeWarps - 1) / kRopeWarps;
+  p.n_split = (steps + kRopeBatch - 1) / kRopeBatch;
+  p.steps_per_warp = (steps + p.n_split - 1) / p.n_split;
+  const long long gx = (long long)p.tok_blocks * p.n_split;
+  if (gx > 0x7fffffffLL || d.batch > 65535) return cudaErrorNotSupported;
+  const dim3 grid((unsigned)gx, (unsigned)d.batch);
+  if (d.dtype == HATA_BF16) {
+    if (a.interleaved) launch_rope_t<__nv_bfloat16, true>(p, pg != nullptr, grid, st);
+    else launch_rope_t<__nv_bfloat16, false>(p, pg != nullptr, grid, st);
+  } else {
+    if (a.interleaved) launch_rope_t<float, true>(p, pg != nullptr, grid, st);
+    else launch_rope_t<float, false>(p, pg != nullptr, grid, st);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace hata

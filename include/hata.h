@@ -77,7 +77,8 @@ typedef enum {
   HATA_ERR_UNSUPPORTED = 2, /* valid but not implemented (e.g. head_dim != 128) */
   HATA_ERR_CUDA = 3,        /* a CUDA launch or runtime call failed */
   HATA_ERR_TIMEOUT = 4,     /* a bounded device-side wait gave up */
-  HATA_ERR_WORKSPACE = 5    /* workspace missing or smaller than hata_workspace_size */
+  HATA_ERR_WORKSPACE = 5,   /* workspace missing or smaller than hata_workspace_size */
+  HATA_ERR_NO_PAGES = 6     /* hata_pages_resize: the pool has too few free pages */
 } hata_status_t;
 
 typedef enum { HATA_F32 = 0, HATA_BF16 = 1 } hata_dtype_t;
@@ -325,6 +326,160 @@ HATA_API hata_status_t hata_prefill_workspace_size(const hata_dims_t* dims, size
 HATA_API hata_status_t hata_prefill_attention(const hata_dims_t* dims, const void* q, const void* K, const void* V,
                                      const float* W_H, void* codes, const int32_t* seq_lens, float scale, void* out,
                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Norms of queries and keys for each head, the position rotation and the cache
+ * append in one pass over a projection's output: what stands between the
+ * projection and a decode step, a prefill or a tree attention.  For token
+ * i < n_b of sequence b (n_b = n_new[b], or n_tok if n_new is NULL), with cache slot
+ * s = seq_lens[b] - n_b + i and rotary position t = positions[b][i] (NULL: s):
+ *     y = x * rsqrt(mean(x^2) + eps) * w                         (weight NULL: y = x)
+ *     (y_a, y_c) -> (y_a cos - y_c sin, y_c cos + y_a sin)       for the rot_dim / 2 pairs
+ *     q_out[b][h][i] = y of q_in[b][i][h],  K[b][g][s] = y of k_in[b][i][g],
+ *     V[b][g][s] = v_in[b][i][g]
+ * computed in fp32 and rounded once.  Pairs are elements (e, e + rot_dim / 2) of
+ * the first rot_dim, or (2 e, 2 e + 1) when `interleaved` is not 0; the other
+ * elements are only normed.
+ *   q_in, k_in, v_in  device, dims->dtype: token (b, i) at element (b * n_tok + i)
+ *                     * stride, its heads [Hq or Hkv][d] contiguous; strides in
+ *                     elements, at least heads * d and a multiple of 16 bytes, so the
+ *                     three may be parts of one projection's output
+ *   q_weight, k_weight  device [d] fp32, or NULL for no norm
+ *   eps               > 0 and finite
+ *   table             device [n_pos][2][rot_dim / 2] fp32, cosines then sines
+ *                     (hata_rope_table, or any the caller makes); NULL if rot_dim = 0
+ *   rot_dim           0 (no rotation) or a multiple of 16, at most d
+ *   q_out             device [B][Hq][n_tok][d]; rows i >= n_b are left as they were
+ *   K, V              the caches of hata_decode_step (pools and table of
+ *                     hata_decode_step_paged in the paged form)
+ *   workspace         at least 16 bytes: its status word
+ * A sequence with n_b outside [0, n_tok] or seq_lens[b] outside [n_b, max_seq], a
+ * token whose position lies outside [0, n_pos), and the cache rows of a token whose
+ * block number lies outside the pool are left unwritten and flagged in the status
+ * word.  Inputs and outputs must not overlap.  batch at most 65535.
+ */
+HATA_API hata_status_t hata_norm_rope(const hata_dims_t* dims, int n_tok, const void* q_in, long long q_stride,
+                                      const void* k_in, long long k_stride, const void* v_in, long long v_stride,
+                                      const float* q_weight, const float* k_weight, float eps, const float* table,
+                                      int n_pos, int rot_dim, int interleaved, const int32_t* n_new,
+                                      const int32_t* positions, const int32_t* seq_lens, void* q_out, void* K, void* V,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+HATA_API hata_status_t hata_norm_rope_paged(const hata_dims_t* dims, int n_tok, const void* q_in, long long q_stride,
+                                            const void* k_in, long long k_stride, const void* v_in, long long v_stride,
+                                            const float* q_weight, const float* k_weight, float eps,
+                                            const float* table, int n_pos, int rot_dim, int interleaved,
+                                            const int32_t* n_new, const int32_t* positions, const int32_t* seq_lens,
+                                            void* q_out, void* K_pool, void* V_pool, const int32_t* block_table,
+                                            int block_size, int n_blocks, void* workspace, size_t workspace_bytes,
+                                            void* stream);
+
+/* Fills table [n_pos][2][rot_dim / 2] (fp32, device) with the cosines and sines of
+ * t * theta^(-2 i / rot_dim), the angles in fp64.  Made once per model.  rot_dim a
+ * multiple of 16 in [16, d = 128], theta > 0 and finite. */
+HATA_API hata_status_t hata_rope_table(float* table, int n_pos, int rot_dim, double theta, void* stream);
+
+/* Bytes of workspace for hata_window_decode and hata_tree_attention (and their paged
+ * forms) with n_tok new tokens per sequence (1 for a window decode); 16-byte
+ * aligned; zeroed once with hata_workspace_init before the first call, and every
+ * call leaves its counters at zero.  One workspace serves one call at a time. */
+HATA_API hata_status_t hata_span_workspace_size(const hata_dims_t* dims, int n_tok, size_t* bytes);
+
+/*
+ * Decode attention with a sliding window and a few first tokens that stay visible,
+ * for layers that keep no top-k: with L_b = seq_lens[b], query head h in group g sees slot s
+ * iff s < L_b and (s < n_sink or s >= L_b - window):
+ *     out[b][h] = sum_s softmax_s(scale * q[b][h] . K[b][g][s]) V[b][g][s]
+ * Layouts of hata_dense_decode; fp32 or bf16, any G.  window >= 1, n_sink >= 0; scale
+ * <= 0 selects 1/sqrt(d).  An empty sequence (L_b <= 0) gives zeros; L_b > max_seq is
+ * clamped and flagged.  Slots that are not visible may hold anything.  In the paged form a
+ * block number outside the pool is replaced by block 0 and flagged.  bf16 probabilities
+ * are rounded to bf16 for P.V with fp32 accumulation, as in hata_dense_decode.
+ */
+HATA_API hata_status_t hata_window_decode(const hata_dims_t* dims, const void* q, const void* K, const void* V,
+                                          const int32_t* seq_lens, int window, int n_sink, float scale, void* out,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+HATA_API hata_status_t hata_window_decode_paged(const hata_dims_t* dims, const void* q, const void* K_pool,
+                                                const void* V_pool, const int32_t* block_table, int block_size,
+                                                int n_blocks, const int32_t* seq_lens, int window, int n_sink,
+                                                float scale, void* out, void* workspace, size_t workspace_bytes,
+                                                void* stream);
+
+/*
+ * Attention of n_tok drafted tokens per sequence over a cache that already holds them
+ * (hata_norm_rope wrote them): the verification of speculative decoding.  With
+ * L_b = seq_lens[b] including them, n_b = n_new[b] of them (NULL: n_tok) and
+ * ctx = L_b - n_b, token i < n_b sees slot s iff s < ctx, or s < L_b and bit (s - ctx)
+ * of mask[b][i] is set (mask NULL: s - ctx <= i, a chain):
+ *     out[b][h][i] = sum_s softmax_s(scale * q[b][h][i] . K[b][g][s]) V[b][g][s]
+ *   q, out   device [B][Hq][n_tok][d]; rows i >= n_b of out are left as they were
+ *   mask     device [B][n_tok][ceil(n_tok / 32)] uint32, bit j % 32 of word j / 32
+ *            for token j; bits of tokens j >= n_b are ignored
+ *   n_tok    1 .. 128
+ * A token that sees nothing gives zeros.  Slots that no token sees may hold anything;
+ * a value row that some token sees must be finite.  A sequence with n_b outside
+ * [0, n_tok] or L_b outside [n_b, max_seq] is flagged and its rows left as they were.
+ * scale, types, paging and rounding as in hata_window_decode.
+ */
+HATA_API hata_status_t hata_tree_attention(const hata_dims_t* dims, int n_tok, const void* q, const void* K,
+                                           const void* V, const int32_t* seq_lens, const int32_t* n_new,
+                                           const uint32_t* mask, float scale, void* out, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+HATA_API hata_status_t hata_tree_attention_paged(const hata_dims_t* dims, int n_tok, const void* q, const void* K_pool,
+                                                 const void* V_pool, const int32_t* block_table, int block_size,
+                                                 int n_blocks, const int32_t* seq_lens, const int32_t* n_new,
+                                                 const uint32_t* mask, float scale, void* out, void* workspace,
+                                                 size_t workspace_bytes, void* stream);
+
+/*
+ * Bookkeeping of a paged cache, on the device and in stream order.  block_table is
+ * [B][ceil(max_seq / block_size)] with -1 where a sequence has no page; seq_lens [B];
+ * ref_count [n_blocks] counts the table entries that name a page, and a page with count 0
+ * is free.  The caller starts with all entries -1 and all counts and lengths 0 (or with any
+ * consistent state).  All are int32 on the device.  At most 1024 sequences.  The
+ * workspace (hata_pages_workspace_size bytes, 16-byte aligned) needs no initialisation apart from its
+ * status word.
+ *
+ * hata_pages_fork: row b takes the pages and the length of row parent[b] as they were before the
+ * call (all rows at once, so beams may be permuted); its own pages are released.  parent[b] < 0 or = b
+ * leaves row b as it is; parent[b] >= B is flagged and does too.  No rows of the cache are copied:
+ * pages are shared until hata_pages_resize grows a row.
+ *
+ * hata_pages_resize: brings every sequence to new_lens[b].  First all pages past the new
+ * ends are released; then, for each growing sequence in order, a partly filled last page that
+ * others share is replaced by a copy of its own (K, V and, if codes_pool is not NULL, codes),
+ * and pages are added.  The lowest free pages are taken first.  If the pool has too few free pages,
+ * HATA_ERR_NO_PAGES is recorded and no sequence grows (their lengths tell).  new_lens[b] or
+ * seq_lens[b] outside [0, max_seq] is flagged and leaves the row as it is.  Length 0 frees a sequence.
+ */
+HATA_API hata_status_t hata_pages_workspace_size(const hata_dims_t* dims, size_t* bytes);
+HATA_API hata_status_t hata_pages_fork(const hata_dims_t* dims, const int32_t* parent, int32_t* block_table,
+                                       int block_size, int n_blocks, int32_t* seq_lens, int32_t* ref_count,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+HATA_API hata_status_t hata_pages_resize(const hata_dims_t* dims, const int32_t* new_lens, void* K_pool, void* V_pool,
+                                         void* codes_pool, int32_t* block_table, int block_size, int n_blocks,
+                                         int32_t* seq_lens, int32_t* ref_count, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/*
+ * Accepted rows moved to the front of the newest n_b tokens (after a tree attention, or
+ * to drop any of the newest tokens): with base = seq_lens[b] - n_b, for j < n_keep[b]
+ * rows base + keep[b][j] of K, V and, if not NULL, codes go to base + j, and
+ * new_lens[b] = base + n_keep[b] (new_lens may be NULL and must not be seq_lens).
+ *   keep   device [B][n_tok] int32, its first n_keep[b] strictly ascending in [0, n_b)
+ *   n_new  device [B] int32, or NULL for n_tok; n_tok in [1, max_seq]
+ * seq_lens is not changed (the paged form's pages are released by hata_pages_resize to
+ * new_lens).  A sequence whose keep or lengths break these rules is flagged and left as it is
+ * (new_lens[b] = seq_lens[b]); rows in blocks outside the pool are flagged and skipped.  The workspace
+ * is at least 16 bytes: its status word.
+ */
+HATA_API hata_status_t hata_compact_kv(const hata_dims_t* dims, int n_tok, const int32_t* keep, const int32_t* n_keep,
+                                       const int32_t* n_new, const int32_t* seq_lens, void* K, void* V, void* codes,
+                                       int32_t* new_lens, void* workspace, size_t workspace_bytes, void* stream);
+HATA_API hata_status_t hata_compact_kv_paged(const hata_dims_t* dims, int n_tok, const int32_t* keep,
+                                             const int32_t* n_keep, const int32_t* n_new, const int32_t* seq_lens,
+                                             void* K_pool, void* V_pool, void* codes_pool, const int32_t* block_table,
+                                             int block_size, int n_blocks, int32_t* new_lens, void* workspace,
+                                             size_t workspace_bytes, void* stream);
 
 /*
  * hata_topk without a workspace, for callers that cannot allocate device memory
