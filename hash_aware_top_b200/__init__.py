@@ -50,6 +50,7 @@ __all__ = [
     "hata_span_workspace_size",
     "hata_window_decode",
     "hata_window_decode_paged",
+    "hata_window_prefill",
     "hata_tree_attention",
     "hata_tree_attention_paged",
     "hata_pages_workspace_size",
@@ -98,6 +99,7 @@ EXPORTED_SYMBOLS = (
     "hata_span_workspace_size",
     "hata_window_decode",
     "hata_window_decode_paged",
+    "hata_window_prefill",
     "hata_tree_attention",
     "hata_tree_attention_paged",
     "hata_pages_workspace_size",
@@ -179,6 +181,7 @@ def _load():
         "hata_span_workspace_size": (I, [DP, I, ctypes.POINTER(S)]),
         "hata_window_decode": (I, [DP, P, P, P, P, I, I, F, P, P, S, P]),
         "hata_window_decode_paged": (I, [DP, P, P, P, P, I, I, P, I, I, F, P, P, S, P]),
+        "hata_window_prefill": (I, [DP, P, P, P, P, I, I, F, P, P, S, P]),
         "hata_tree_attention": (I, [DP, I, P, P, P, P, P, P, F, P, P, S, P]),
         "hata_tree_attention_paged": (I, [DP, I, P, P, P, P, I, I, P, P, P, F, P, P, S, P]),
         "hata_pages_workspace_size": (I, [DP, ctypes.POINTER(S)]),
@@ -627,6 +630,19 @@ def hata_window_decode_paged(dims: Dims, q, K_pool, V_pool, block_table, block_s
             _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32), int(window), int(n_sink), float(scale),
             _dptr(out, "out", row, d.torch_dtype), *_ws(ws), _stream(stream)),
         "hata_window_decode_paged")
+
+
+def hata_window_prefill(dims: Dims, q, K, V, seq_lens, window, n_sink, scale, out, ws, stream=None):
+    """Causal prefill attention (q/out [B][Hq][max_seq][d], K/V [B][Hkv][max_seq][d], bf16) over the last `window`
+    positions and the first `n_sink`."""
+    d = dims
+    rows = (d.batch, d.n_q_heads, d.max_seq, d.head_dim)
+    _check(
+        lib.hata_window_prefill(
+            ctypes.byref(d), _dptr(q, "q", rows, d.torch_dtype), *_cache_args(d, K, V),
+            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32), int(window), int(n_sink), float(scale),
+            _dptr(out, "out", rows, d.torch_dtype), *_ws(ws), _stream(stream)),
+        "hata_window_prefill")
 
 
 def _tree_args(d, q, seq_lens, n_new, mask, out):

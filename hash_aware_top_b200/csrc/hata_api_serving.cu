@@ -138,6 +138,20 @@ hata_status_t hata_window_decode_paged(const hata_dims_t* dims, const void* q, c
   return span_call(dims, a, &pg, workspace, workspace_bytes, stream);
 }
 
+hata_status_t hata_window_prefill(const hata_dims_t* dims, const void* q, const void* K, const void* V,
+                                  const int32_t* seq_lens, int window, int n_sink, float scale, void* out,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+  hata_status_t s = check_dims(dims);
+  if (s != HATA_OK) return s;
+  if (dims->dtype != HATA_BF16) return HATA_ERR_UNSUPPORTED;
+  if (!ok16(q) || !ok16(K) || !ok16(V) || !ok16(out) || !ok4(seq_lens)) return HATA_ERR_INVALID_ARG;
+  if (window < 1 || n_sink < 0 || !std::isfinite(scale)) return HATA_ERR_INVALID_ARG;
+  if (!ok16(workspace) || workspace_bytes < kStatusBytes) return HATA_ERR_WORKSPACE;
+  if (scale <= 0.f) scale = 1.0f / std::sqrt((float)dims->head_dim);
+  return status_of(launch_window_prefill(*dims, q, K, V, seq_lens, window, n_sink, scale, out,
+                                         static_cast<uint32_t*>(workspace), static_cast<cudaStream_t>(stream)));
+}
+
 hata_status_t hata_tree_attention(const hata_dims_t* dims, int n_tok, const void* q, const void* K, const void* V,
                                   const int32_t* seq_lens, const int32_t* n_new, const uint32_t* mask, float scale,
                                   void* out, void* workspace, size_t workspace_bytes, void* stream) {

@@ -77,6 +77,11 @@ struct SpanArgs {
 constexpr int kMaxTreeTokens = 128;  // new tokens per sequence of one call
 size_t span_ws_bytes(const hata_dims_t& d, int n_tok);
 cudaError_t launch_span(const hata_dims_t& d, const SpanArgs& a, const PagedCache* pg, char* ws, cudaStream_t stream);
+int span_sms();  // SMs of the current device, found once per device
+// Prefill with a sliding window and sinks (hata_span_tc.cu).
+cudaError_t launch_window_prefill(const hata_dims_t& d, const void* q, const void* K, const void* V,
+                                  const int32_t* seq_lens, int window, int sink, float scale, void* out,
+                                  uint32_t* status, cudaStream_t stream);
 
 // Page bookkeeping and row compaction (hata_pages.cu).
 constexpr int kMaxPageRows = 1024;  // sequences of one call

@@ -274,27 +274,6 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_simt_kernel(const Params p
   }
 }
 
-int sm_count() {
-  static std::mutex mu;
-  static std::map<int, int> cache;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return 148;
-  }
-  std::lock_guard<std::mutex> lk(mu);
-  auto it = cache.find(dev);
-  if (it == cache.end()) {
-    int sms = 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
-      (void)cudaGetLastError();
-      sms = 148;
-    }
-    it = cache.emplace(dev, sms).first;
-  }
-  return it->second;
-}
-
 // Shared-memory attribute of a kernel, set once per device under a mutex; a failed call is returned on
 // every later launch on that device.
 template <typename Kernel>
@@ -320,7 +299,7 @@ cudaError_t launch_simt(Params p, cudaStream_t st) {
   cudaError_t e = configure(span_simt_kernel<T, ROWS, PAGED>, smem);
   if (e != cudaSuccess) return e;
   p.row_tiles = (p.R + ROWS - 1) / ROWS;
-  span_simt_kernel<T, ROWS, PAGED><<<sm_count(), kSpThreads, smem, st>>>(p);
+  span_simt_kernel<T, ROWS, PAGED><<<span_sms(), kSpThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -338,10 +317,38 @@ size_t count_bytes(const hata_dims_t& d, int n_tok) {
   return align_up((size_t)d.batch * d.n_kv_heads * ((R + kSpanMinRows - 1) / kSpanMinRows) * 4, kAlign);
 }
 
+// bf16 with more rows per KV head than this runs on the tensor cores.
+constexpr int kSpanTcRows = 16;
+bool use_tc(const hata_dims_t& d, int n_tok) {
+  return d.dtype == HATA_BF16 && (d.n_q_heads / d.n_kv_heads) * n_tok > kSpanTcRows;
+}
+
 }  // namespace
 
+int span_sms() {
+  static std::mutex mu;
+  static std::map<int, int> cache;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 148;
+  }
+  std::lock_guard<std::mutex> lk(mu);
+  auto it = cache.find(dev);
+  if (it == cache.end()) {
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+      (void)cudaGetLastError();
+      sms = 148;
+    }
+    it = cache.emplace(dev, sms).first;
+  }
+  return it->second;
+}
+
 size_t span_ws_bytes(const hata_dims_t& d, int n_tok) {
-  return kAlign + count_bytes(d, n_tok) + (size_t)sm_count() * 2 * kSpanMaxRows * (kHeadDim + 2) * 4;
+  const size_t simt = (size_t)span_sms() * 2 * kSpanMaxRows * (kHeadDim + 2) * 4;
+  return kAlign + count_bytes(d, n_tok) + (use_tc(d, n_tok) ? std::max(simt, span_tc_part_bytes(d, n_tok)) : simt);
 }
 
 cudaError_t launch_span(const hata_dims_t& d, const SpanArgs& a, const PagedCache* pg, char* ws, cudaStream_t st) {
@@ -373,6 +380,7 @@ cudaError_t launch_span(const hata_dims_t& d, const SpanArgs& a, const PagedCach
     p.n_blocks = pg->n_blocks;
     p.max_blocks = pg->max_blocks;
   }
+  if (a.window == 0 && use_tc(d, a.n_tok)) return launch_span_tc(d, p, pg, st);
   if (d.dtype == HATA_BF16) return launch_simt_t<__nv_bfloat16>(p, st);
   return launch_simt_t<float>(p, st);
 }

@@ -166,4 +166,8 @@ __device__ __forceinline__ void store_out<__nv_bfloat16>(__nv_bfloat16* out, flo
 
 }  // namespace span
 
+// Tensor-core form of tree attention (hata_span_tc.cu): bf16, any number of rows.
+size_t span_tc_part_bytes(const hata_dims_t& d, int n_tok);
+cudaError_t launch_span_tc(const hata_dims_t& d, const span::Params& s, const PagedCache* pg, cudaStream_t stream);
+
 }  // namespace hata

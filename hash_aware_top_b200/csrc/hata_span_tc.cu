@@ -1,0 +1,753 @@
+// Attention on the 5th-generation tensor cores where many query rows share their keys: prefill with a
+// sliding window and sinks, and tree attention when a KV head has many (query head, token) rows.
+//
+// A CTA (ten warps, one per SM, persistent) runs two streams.  A stream is 128 query rows with their
+// own scores S and output O in TMEM (128 columns each) and a warpgroup whose thread owns one row:
+//   S = Q K^T (tcgen05.mma, M = N = 128)  ->  p = 2^(s c - m), c = scale log2 e, in registers  ->  P as bf16 over
+//   the first half of S  ->  O += P V (P from TMEM, V as an MN-major operand)
+// While one stream's warpgroup computes its exponentials, the tensor core works for the other.  K and V tiles of
+// 128 slots come through one ring of five 32 KB stages (TMA; a page of fewer than 128 slots is a box of its own);
+// one warp loads, one lane of another issues the MMAs.  The running maximum m moves only when a row's maximum
+// passes it by more than 2^8; O is then rescaled in TMEM, which is safe once S has arrived, since the MMAs run in
+// order and PV of the tile before was issued first.
+//
+// The two streams take
+//   * prefill: 256 rows = P heads of one group x 256 / P positions, P the largest power of two in G (at most
+//     16), so a window's ragged ends cost 256 / P rows, not 256;
+//   * tree, more than 128 rows: two tiles of rows, every key tile read by both;
+//   * tree, up to 128 rows: the same rows, even key tiles for one stream, odd ones for the other.
+// Prefill writes its rows.  Tree attention splits the key tiles of all units evenly over the CTAs (hata_span.cuh);
+// each run of a unit leaves (maximum, sum, O) in fp32 in the workspace, and span_merge_kernel joins them in
+// the order of the split.
+//
+// Every wait is bounded; on expiry HATA_ERR_TIMEOUT goes to the status word, and the CTA stops issuing,
+// waits (bounded) for its copies and MMAs, frees its TMEM and returns.
+#include <algorithm>
+#include <map>
+#include <mutex>
+
+#include "hata_span.cuh"
+#include "hata_tc.cuh"
+
+namespace hata {
+
+namespace {
+
+using span::Params;
+
+constexpr int kTcThreads = 320;
+constexpr int kTcMmaWarp = 8, kTcTmaWarp = 9;
+constexpr int kTcTile = 128;
+static_assert(kTcTile == span::kSpanTile, "the split of the work counts these tiles");
+constexpr int kTcTileB = kTcTile * kHeadDim * 2;  // 32 KB
+constexpr int kTcStages = 5;
+constexpr uint32_t kTcQ = 0;                      // two tiles of query rows
+constexpr uint32_t kTcRing = 2 * kTcTileB;
+constexpr int kTcSmem = (2 + kTcStages) * kTcTileB + 1024;  // + alignment to 1024 bytes
+constexpr uint32_t kTcTmemCols = 512;             // S of the streams at 0 and 128, O at 256 and 384
+constexpr uint32_t kTcTries = 1u << 22, kTcTestTries = 1u << 10;
+constexpr float kTcSlack = 8.f;  // log2 units: p <= 2^8 between rescales
+constexpr int kPartFloats = kTcTile * (kHeadDim + 2);  // a stream's partial: m [128], l [128], O [32][128][4]
+
+struct TcParams {
+  Params s;
+  int prefill_heads;  // P: heads of a prefill CTA
+  int pos_block;      // prefill: positions of a CTA (256 / P)
+  int n_blocks_pos;   // prefill: blocks of positions
+  int pair;           // tree: two tiles of rows (else one, its key tiles shared out)
+  int box_rows;       // rows of a K / V box
+  int q_box;          // rows of a Q box
+  int test_expire;
+};
+
+// One CTA's next piece of work: a run of key tiles for its two streams.
+struct Seg {
+  int b, g;
+  int L, ctx, n_b;
+  int sink_tiles, win_tile;  // list index j -> tile
+  int j0, j1;                // run of the list
+  int row0;                  // tree: first row; prefill: first position
+  int head0;                 // prefill: first query head
+  long long slot;            // tree: partial
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Walks the pieces of work of a CTA.  All lanes of a warp call it together; every warp walks alike.
+template <bool TREE>
+struct Walk {
+  const TcParams& p;
+  int lane;
+  long long at, end, per;
+  span::Cursor cur;
+
+  __device__ __forceinline__ Walk(const TcParams& prm, int ln, bool flag) : p(prm), lane(ln) {
+    if constexpr (TREE) {
+      const long long total = span::total_tiles(p.s, lane, flag);
+      per = max(1LL, (total + gridDim.x - 1) / gridDim.x);
+      at = (long long)blockIdx.x * per;
+      end = min(total, at + per);
+      if (at < end) cur = span::find(p.s, at, lane);
+    } else {
+      if (flag)
+        for (int b = lane; b < p.s.B; b += 32)
+          if (p.s.seq_lens[b] > p.s.max_seq) set_status(p.s.status, HATA_ERR_INVALID_ARG);
+      per = gridDim.x;
+      at = blockIdx.x;
+      end = (long long)p.n_blocks_pos * p.s.B * (p.s.Hq / p.prefill_heads);
+    }
+  }
+
+  __device__ __forceinline__ bool next(Seg& s) {
+    if constexpr (TREE) {
+      if (at >= end) return false;
+      const long long upt = (long long)p.s.Hkv * p.s.row_tiles;
+      while (at >= cur.seq_start + (long long)cur.seq.tiles * upt) {
+        cur.seq_start += (long long)cur.seq.tiles * upt;
+        cur.seq = span::seq_of(p.s, ++cur.b);
+      }
+      const long long in_seq = (at - cur.seq_start) / cur.seq.tiles;
+      const long long u0 = cur.seq_start + in_seq * cur.seq.tiles, u1 = u0 + cur.seq.tiles;
+      s.b = cur.b;
+      s.g = (int)(in_seq % p.s.Hkv);
+      s.L = cur.seq.L;
+      s.ctx = cur.seq.ctx;
+      s.n_b = cur.seq.n_b;
+      s.sink_tiles = s.win_tile = 0;
+      s.j0 = (int)(at - u0);
+      s.j1 = (int)(min(end, u1) - u0);
+      s.row0 = (int)(in_seq / p.s.Hkv) * (p.pair ? 2 * kTcTile : kTcTile);
+      s.head0 = 0;
+      s.slot = (long long)cur.b * upt + in_seq + blockIdx.x;  // unit + CTA: grows along the list of tiles
+      at = u0 + s.j1;
+      return true;
+    } else {
+      for (; at < end; at += per) {
+        const int hb = p.s.Hq / p.prefill_heads;
+        const long long rest = at % ((long long)p.s.B * hb);
+        const int blk = p.n_blocks_pos - 1 - (int)(at / ((long long)p.s.B * hb));  // the longest rows first
+        s.b = (int)(rest / hb);
+        s.head0 = (int)(rest % hb) * p.prefill_heads;
+        s.g = s.head0 / p.s.G;
+        int L = p.s.seq_lens[s.b];
+        L = max(0, min(L, p.s.max_seq));
+        s.row0 = blk * p.pos_block;
+        if (s.row0 >= L) continue;
+        s.L = s.ctx = L;
+        s.n_b = 0;
+        const int t_hi = min(s.row0 + p.pos_block, L) - 1;
+        const int first = max(0, s.row0 - min(p.s.window, s.row0 + 1) + 1) / kTcTile, last = t_hi / kTcTile;
+        s.sink_tiles = min((min(p.s.sink, t_hi + 1) + kTcTile - 1) / kTcTile, first);
+        s.win_tile = first;
+        s.j0 = 0;
+        s.j1 = s.sink_tiles + last - first + 1;
+        s.slot = 0;
+        at += per;
+        return true;
+      }
+      return false;
+    }
+  }
+};
+
+__device__ __forceinline__ int tile_of(const Seg& s, int j) {
+  return j < s.sink_tiles ? j : s.win_tile + j - s.sink_tiles;
+}
+
+// Visibility words of new tokens, 128 bits in four registers; bit j: token j is seen.
+struct Bits128 {
+  uint32_t w0, w1, w2, w3;
+  __device__ __forceinline__ uint32_t word(int i) const {  // ones below (the context), zeros above
+    return i < 0 ? 0xffffffffu : i == 0 ? w0 : i == 1 ? w1 : i == 2 ? w2 : i == 3 ? w3 : 0u;
+  }
+  // bits j0 .. j0 + 31, where negative indices are slots before the new tokens
+  __device__ __forceinline__ uint32_t at(int j0) const {
+    const int i = j0 >> 5;  // floor
+    return __funnelshift_r(word(i), word(i + 1), j0 & 31);
+  }
+};
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+template <bool TREE, bool PAGED>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    span_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap, const TcParams p) {
+  extern __shared__ __align__(1024) unsigned char tc_smem[];
+  __shared__ __align__(8) uint64_t q_full, q_free, full[kTcStages], freed[kTcStages], s_full[2], p_full[2], o_full[2],
+      drain, never;
+  __shared__ uint32_t tmem_s;
+  __shared__ volatile int abort_s;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (tc::smem_u32(tc_smem) + 1023u) & ~1023u;
+  if (warp == 0) tc::tmem_alloc(&tmem_s, kTcTmemCols);
+  if (tid == 256) {
+    tc::mbar_init(&q_full, 1);
+    tc::mbar_init(&q_free, 1);
+    for (int i = 0; i < kTcStages; ++i) {
+      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&freed[i], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      tc::mbar_init(&s_full[w], 1);
+      tc::mbar_init(&p_full[w], kTcTile);
+      tc::mbar_init(&o_full[w], 1);
+    }
+    tc::mbar_init(&drain, 1);
+    tc::mbar_init(&never, 1);
+    tc::mbar_init_fence();
+    abort_s = 0;
+  }
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = tmem_s;
+
+  auto wait_ok = [&](uint64_t* bar, uint32_t parity) -> bool {
+    for (uint32_t it = 0; it < kTcTries; it += 64) {
+      if (abort_s) return false;
+      if (tc::mbar_wait(bar, parity, 64)) return true;
+    }
+    set_status(p.s.status, HATA_ERR_TIMEOUT);
+    abort_s = 1;
+    return false;
+  };
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {  // the same answer in every lane
+    const bool r = wait_ok(bar, parity);
+    return __all_sync(0xffffffffu, r);
+  };
+  // The ring holds K and V tiles in the order of `item` numbers.  Pair: K_j, V_j, K_{j+1}, ...  Shared out: the K
+  // tiles of both streams, then their V tiles, and so on; an odd last tile has no second stream.
+  const bool pair = !TREE || p.pair;
+  auto streams_in = [&](int n, int i) { return pair ? 1 : (2 * i + 1 < n ? 2 : 1); };  // tiles of step i (pair: one)
+  auto steps_of = [&](int n) { return pair ? n : (n + 1) / 2; };
+  // items of a step i of a run of n tiles, counted from the run's first item: K of stream w, V of stream w
+  auto item_k = [&](int i, int w) { return pair ? 2 * i : 4 * i + w; };
+  auto item_v = [&](int n, int i, int w) { return pair ? 2 * i + 1 : 4 * i + streams_in(n, i) + w; };
+
+  Walk<TREE> walk(p, lane, blockIdx.x == 0 && warp == 0);
+  Seg sg;
+
+  if (warp == kTcTmaWarp) {
+    // ---------------- loader: lane l issues box l ----------------
+    uint32_t item = 0;  // ring items issued
+    uint32_t n_q = 0;   // Q loads issued
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      if (n_q > 0 && !(ok = wait_warp(&q_free, (n_q - 1) & 1))) break;
+      ++n_q;
+      if constexpr (TREE) {
+        const int rows = pair ? 2 : 1;
+        if (lane == 0) tc::mbar_expect(&q_full, (uint32_t)(rows * kTcTileB));
+        __syncwarp();
+        const int y = (p.s.Hq * sg.b + sg.g * p.s.G) * p.s.T + sg.row0;
+        if (lane < 2 * rows)
+          tc::tma_load_2d(base + kTcQ + (uint32_t)lane * (kTcTileB / 2), &qmap, 64 * (lane & 1),
+                          y + kTcTile * (lane >> 1), &q_full);
+      } else {
+        if (lane == 0) tc::mbar_expect(&q_full, (uint32_t)(2 * kTcTileB));
+        __syncwarp();
+        // 256 rows as boxes of q_box rows: consecutive heads, or (P = 1) consecutive positions of one head
+        const int boxes = 2 * kTcTile / p.q_box;
+        if (lane < 2 * boxes) {
+          const int bx = lane >> 1, r = bx * p.q_box;  // row of the 256
+          const int head = p.prefill_heads == 1 ? sg.head0 : sg.head0 + bx;
+          const int pos = p.prefill_heads == 1 ? sg.row0 + r : sg.row0;
+          tc::tma_load_2d(base + kTcQ + (uint32_t)(r / kTcTile) * kTcTileB + (uint32_t)(lane & 1) * (kTcTileB / 2) +
+                              (uint32_t)(r % kTcTile) * 128u,
+                          &qmap, 64 * (lane & 1), (p.s.Hq * sg.b + head) * p.s.max_seq + pos, &q_full);
+        }
+      }
+      auto load = [&](const CUtensorMap* map, int tile) -> bool {  // the next ring item
+        const uint32_t st = item % kTcStages, round = item / kTcStages;
+        if (round > 0 && !wait_warp(&freed[st], (round - 1) & 1)) return false;
+        const uint32_t dst = base + kTcRing + st * kTcTileB;
+        const int s0 = tile * kTcTile;
+        if constexpr (PAGED) {
+          // boxes of the pages that hold slots below L; the rows of the others are masked (K) or zeroed (V)
+          const int br = p.box_rows, n_box = min(kTcTile / br, (sg.L - s0 + br - 1) / br);
+          if (lane == 0) tc::mbar_expect(&full[st], (uint32_t)(n_box * br * kHeadDim * 2));
+          __syncwarp();
+          if (lane < 2 * n_box) {
+            const int r = (lane >> 1) * br, s = s0 + r;
+            int blk = p.s.block_table[(size_t)sg.b * p.s.max_blocks + (s >> p.s.block_shift)];
+            if (blk < 0 || blk >= p.s.n_blocks) {
+              set_status(p.s.status, HATA_ERR_INVALID_ARG);
+              blk = 0;
+            }
+            const int y = ((blk * p.s.Hkv + sg.g) << p.s.block_shift) + (s & ((1 << p.s.block_shift) - 1));
+            tc::tma_load_2d(dst + (uint32_t)(lane & 1) * (kTcTileB / 2) + (uint32_t)r * 128u, map, 64 * (lane & 1), y,
+                            &full[st]);
+          }
+        } else {
+          if (lane == 0) tc::mbar_expect(&full[st], (uint32_t)kTcTileB);
+          __syncwarp();
+          if (lane < 2)
+            tc::tma_load_2d(dst + (uint32_t)lane * (kTcTileB / 2), map, 64 * lane,
+                            (p.s.Hkv * sg.b + sg.g) * p.s.max_seq + s0, &full[st]);
+        }
+        ++item;
+        return true;
+      };
+      const int n = sg.j1 - sg.j0, steps = steps_of(n);
+      for (int i = 0; ok && i < steps; ++i) {
+        const int m = streams_in(n, i);
+        for (int w = 0; ok && w < m; ++w) ok = load(&kmap, tile_of(sg, sg.j0 + (pair ? i : 2 * i + w)));
+        for (int w = 0; ok && w < m; ++w) ok = load(&vmap, tile_of(sg, sg.j0 + (pair ? i : 2 * i + w)));
+      }
+    }
+    // every copy still in flight lands before the CTA leaves
+    for (uint32_t it = item > kTcStages ? item - kTcStages : 0; it < item; ++it)
+      tc::mbar_wait(&full[it % kTcStages], (it / kTcStages) & 1, kTcTries);
+    if (n_q > 0) tc::mbar_wait(&q_full, (n_q - 1) & 1, kTcTries);
+  } else if (warp == kTcMmaWarp) {
+    // ---------------- MMA issue ----------------
+    bool ok = true;
+    if (p.test_expire && !tc::mbar_wait(&never, 0, kTcTestTries)) {  // test hook: this wait runs out
+      if (lane == 0) set_status(p.s.status, HATA_ERR_TIMEOUT);
+      abort_s = 1;
+      ok = false;
+    }
+    constexpr uint32_t idS = tc::idesc_bf16(kTcTile, kTcTile, false);
+    constexpr uint32_t idPV = tc::idesc_bf16(kTcTile, kHeadDim, true);
+    uint32_t item0 = 0;       // first ring item of the run
+    uint32_t done[2] = {0, 0};  // tiles whose P this stream has delivered
+    for (int n_seg = 0; ok && walk.next(sg); ++n_seg) {
+      const int n = sg.j1 - sg.j0, steps = steps_of(n);
+      if (lane == 0) {
+        ok = wait_ok(&q_full, (uint32_t)(n_seg & 1));
+        auto wait_item = [&](int k) {
+          const uint32_t it = item0 + (uint32_t)k;
+          return wait_ok(&full[it % kTcStages], (it / kTcStages) & 1);
+        };
+        auto stage_of = [&](int k) { return base + kTcRing + ((item0 + (uint32_t)k) % kTcStages) * kTcTileB; };
+        auto free_item = [&](int k) { tc::commit(&freed[(item0 + (uint32_t)k) % kTcStages]); };
+        auto issue_s = [&](int i, int w) {
+          tc::fence_after();
+          const uint32_t qb = base + kTcQ + (pair ? (uint32_t)w * kTcTileB : 0u), kb = stage_of(item_k(i, w));
+#pragma unroll
+          for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+            const uint32_t off = (uint32_t)((ks >> 2) * (kTcTileB / 2) + (ks & 3) * 32);
+            tc::mma(tmem + (uint32_t)w * kTcTile, tc::desc_kmajor_sw128(qb + off), tc::desc_kmajor_sw128(kb + off), idS,
+                    ks > 0 ? 1u : 0u);
+          }
+          tc::commit(&s_full[w]);
+        };
+        auto issue_pv = [&](int i, int w) {
+          tc::fence_after();
+          const uint32_t vb = stage_of(item_v(n, i, w));
+#pragma unroll
+          for (int ks = 0; ks < kTcTile / 16; ++ks)
+            tc::mma_ts(tmem + 256u + (uint32_t)w * kHeadDim, tmem + (uint32_t)(w * kTcTile + ks * 8),
+                       tc::desc_mnmajor_sw128(vb + (uint32_t)ks * 2048u, (uint32_t)(kTcTileB / 2)), idPV,
+                       (i > 0 || ks > 0) ? 1u : 0u);
+        };
+        const int s0n = pair ? 2 : streams_in(n, 0);  // streams of the first step
+        for (int w = 0; ok && w < s0n; ++w) {
+          if ((!pair || w == 0) && !(ok = wait_item(item_k(0, w)))) break;
+          issue_s(0, w);
+          if (!pair || w == 1) free_item(item_k(0, w));
+        }
+        if (ok && steps == 1) tc::commit(&q_free);
+        for (int i = 0; ok && i < steps; ++i) {
+          const int m = pair ? 2 : streams_in(n, i);
+          const int m_next = i + 1 < steps ? (pair ? 2 : streams_in(n, i + 1)) : 0;
+          for (int w = 0; ok && w < m; ++w) {
+            if (!(ok = wait_ok(&p_full[w], done[w] & 1))) break;
+            ++done[w];
+            if ((!pair || w == 0) && !(ok = wait_item(item_v(n, i, w)))) break;
+            issue_pv(i, w);
+            if (!pair || w == 1) free_item(item_v(n, i, w));
+            if (w < m_next) {
+              if ((!pair || w == 0) && !(ok = wait_item(item_k(i + 1, w)))) break;
+              issue_s(i + 1, w);
+              if (!pair || w == 1) free_item(item_k(i + 1, w));
+              if (i + 2 == steps && w == m_next - 1) tc::commit(&q_free);
+            } else {
+              tc::commit(&o_full[w]);  // the stream's last PV
+            }
+          }
+        }
+        item0 += (uint32_t)(2 * n);
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+    }
+    if (lane == 0) {
+      tc::commit(&drain);  // every MMA issued above completes before the CTA leaves
+      tc::mbar_wait(&drain, 0, kTcTries);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- a stream's warpgroup: row m of its 128 ----------------
+    const int w = warp >> 2, m = tid & 127;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t sa = lane_base + (uint32_t)(w * kTcTile), oa = lane_base + 256u + (uint32_t)(w * kHeadDim);
+    const float c = p.s.scale_log2;
+    uint32_t item0 = 0, tiles = 0, outs = 0;  // ring items, score tiles and outputs so far
+    bool ok = true;
+    while (ok && walk.next(sg)) {
+      const int n = sg.j1 - sg.j0, steps = steps_of(n);
+      const int mine = pair ? steps : (n + 1 - w) / 2;  // steps of this stream
+      // what this row sees
+      int t = 0, row = 0;
+      bool live;
+      Bits128 seen{0u, 0u, 0u, 0u}, any{0u, 0u, 0u, 0u};
+      const bool has_new = TREE && sg.j1 * kTcTile > sg.ctx;  // the run reaches the new tokens
+      if constexpr (TREE) {
+        row = sg.row0 + (pair ? w * kTcTile : 0) + m;
+        const int i = row % p.s.T;
+        live = row < p.s.R && i < sg.n_b;
+        if (has_new) {
+          if (p.s.mask) {
+            const uint32_t* mw = p.s.mask + ((size_t)sg.b * p.s.T + i) * p.s.mask_words;
+            seen.w0 = mw[0];
+            if (p.s.mask_words > 1) seen.w1 = mw[1];
+            if (p.s.mask_words > 2) seen.w2 = mw[2];
+            if (p.s.mask_words > 3) seen.w3 = mw[3];
+          } else {
+            seen.w0 = below(i + 1);
+            seen.w1 = below(i - 31);
+            seen.w2 = below(i - 63);
+            seen.w3 = below(i - 95);
+          }
+          seen.w0 &= below(sg.n_b);
+          seen.w1 &= below(sg.n_b - 32);
+          seen.w2 &= below(sg.n_b - 64);
+          seen.w3 &= below(sg.n_b - 96);
+          // the new tokens that any token sees
+          any = {0u, 0u, 0u, 0u};
+          for (int j = lane; p.s.mask && j < sg.n_b; j += 32) {
+            const uint32_t* mw = p.s.mask + ((size_t)sg.b * p.s.T + j) * p.s.mask_words;
+            any.w0 |= mw[0];
+            if (p.s.mask_words > 1) any.w1 |= mw[1];
+            if (p.s.mask_words > 2) any.w2 |= mw[2];
+            if (p.s.mask_words > 3) any.w3 |= mw[3];
+          }
+          any.w0 = __reduce_or_sync(0xffffffffu, p.s.mask ? any.w0 : 0xffffffffu) & below(sg.n_b);
+          any.w1 = __reduce_or_sync(0xffffffffu, p.s.mask ? any.w1 : 0xffffffffu) & below(sg.n_b - 32);
+          any.w2 = __reduce_or_sync(0xffffffffu, p.s.mask ? any.w2 : 0xffffffffu) & below(sg.n_b - 64);
+          any.w3 = __reduce_or_sync(0xffffffffu, p.s.mask ? any.w3 : 0xffffffffu) & below(sg.n_b - 96);
+        }
+      } else {
+        t = p.prefill_heads == 1 ? sg.row0 + w * kTcTile + m : sg.row0 + m % p.pos_block;
+        live = t < sg.L;
+      }
+      float m_used = -INFINITY, l = 0.f;
+      for (int i = 0; i < mine; ++i) {
+        const int tile = tile_of(sg, sg.j0 + (pair ? i : 2 * i + w)), s0 = tile * kTcTile;
+        if (!(ok = wait_warp(&s_full[w], tiles & 1))) break;
+        ++tiles;
+        tc::fence_after();
+        uint32_t x[4][32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc::ld32_nowait(sa + 32 * k, x[k]);
+        tc::ld_wait();
+        const uint32_t ninf = 0xff800000u;
+        if constexpr (TREE) {
+          if (s0 + kTcTile > sg.ctx) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t v = seen.at(s0 + 32 * k - sg.ctx);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[k][e] = (v >> e) & 1u ? x[k][e] : ninf;
+            }
+          }
+        } else {
+          // visible: e <= hi and (e >= lo or e < sk)
+          const int hi = t - s0, lo = t - min(p.s.window, t + 1) + 1 - s0, sk = min(p.s.sink, sg.L) - s0;
+          if (__any_sync(0xffffffffu, hi < kTcTile - 1 || (lo > 0 && sk < kTcTile))) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const int ee = 32 * k + e;
+                x[k][e] = (ee <= hi && (ee >= lo || ee < sk)) ? x[k][e] : ninf;
+              }
+          }
+        }
+        float mx[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          mx[k] = __uint_as_float(x[k][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) mx[k] = fmaxf(mx[k], __uint_as_float(x[k][e]));
+        }
+        const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        if (i == 0) {
+          m_used = m_tile;
+        } else if (__any_sync(0xffffffffu, m_tile > m_used + kTcSlack)) {
+          const float m_new = fmaxf(m_used, m_tile);
+          const float alpha = m_new == -INFINITY ? 1.f : ex2(m_used - m_new);
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            uint32_t o[32];
+            tc::ld32(oa + 32 * k, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::st32(oa + 32 * k, o);
+          }
+          l *= alpha;
+          m_used = m_new;
+        }
+        const float mr = m_used == -INFINITY ? 0.f : m_used;  // nothing seen yet: p = 2^-inf = 0
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float pr = ex2(fmaf(__uint_as_float(x[k][e]), c, -mr));
+            sum[e & 3] += pr;
+            x[k][e] = __float_as_uint(pr);
+          }
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            pk[e] = bf16x2(__uint_as_float(x[2 * k][2 * e]), __uint_as_float(x[2 * k][2 * e + 1]));
+            pk[16 + e] = bf16x2(__uint_as_float(x[2 * k + 1][2 * e]), __uint_as_float(x[2 * k + 1][2 * e + 1]));
+          }
+          tc::st32(sa + 32 * k, pk);
+        }
+        tc::st_wait();
+        // value rows that nobody sees (possibly not finite) are zeroed, so that 0 * V stays 0; in a pair the
+        // first stream does it for both, since its PV is issued first
+        if ((!pair || w == 0) && s0 + kTcTile > sg.ctx) {
+          const uint32_t it = item0 + (uint32_t)item_v(n, i, w);
+          if (!(ok = wait_warp(&full[it % kTcStages], (it / kTcStages) & 1))) break;
+          bool drop = s0 + m >= sg.L;
+          if constexpr (TREE) {
+            const int j = s0 + m - sg.ctx;
+            if (!drop && j >= 0) drop = !(any.at(j) & 1u);
+          }
+          if (drop) {
+            unsigned char* vrow = tc_smem + (base - tc::smem_u32(tc_smem)) + kTcRing + (it % kTcStages) * kTcTileB +
+                                  (m >> 3) * 1024 + (m & 7) * 128;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              *reinterpret_cast<uint4*>(vrow + q * 16) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(vrow + kTcTileB / 2 + q * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          tc::fence_async_smem();
+        }
+        tc::fence_before();
+        tc::mbar_arrive(&p_full[w]);
+      }
+      item0 += (uint32_t)(2 * n);
+      if (!ok) break;
+      if (mine > 0) {
+        if (!(ok = wait_warp(&o_full[w], outs & 1))) break;
+        ++outs;
+        tc::fence_after();
+      }
+      if constexpr (TREE) {
+        float* part = p.s.part + ((size_t)sg.slot * 2 + w) * kPartFloats;
+        part[m] = m_used;
+        part[kTcTile + m] = l;
+        if (mine > 0) {
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            uint32_t o[32];
+            tc::ld32(oa + 32 * k, o);
+            float4* dst = reinterpret_cast<float4*>(part + 2 * kTcTile) + (size_t)(8 * k) * kTcTile + m;
+            if (live)
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                dst[q * kTcTile] = make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]),
+                                               __uint_as_float(o[4 * q + 2]), __uint_as_float(o[4 * q + 3]));
+          }
+        }
+      } else {
+        const int head = p.prefill_heads == 1 ? sg.head0
+                                              : sg.head0 + w * (p.prefill_heads / 2) + m / p.pos_block;
+        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.s.out) +
+                              ((size_t)(sg.b * p.s.Hq + head) * p.s.max_seq + t) * kHeadDim;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          uint32_t o[32];
+          tc::ld32(oa + 32 * k, o);
+          if (live) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[e] = bf16x2(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4*>(orow + 32 * k + 8 * q) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          }
+        }
+      }
+      tc::fence_before();  // O has been read: the next run's first P allows its overwriting
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after();
+    tc::tmem_dealloc(tmem, kTcTmemCols);
+  }
+}
+
+// Joins the partials of a unit: thread (row, 4 columns), partials in the order of the split.  grid = (units, 16).
+constexpr int kMergeCols = 2;  // column quads of a CTA
+__global__ void __launch_bounds__(kTcTile* kMergeCols) span_merge_kernel(const TcParams p, int grid_tc, int rows_per_unit) {
+  const int lane = threadIdx.x & 31;
+  const long long upt = (long long)p.s.Hkv * p.s.row_tiles;
+  const long long unit = blockIdx.x;
+  const int b = (int)(unit / upt);
+  const long long in_seq = unit % upt;
+  const span::Seq sq = span::seq_of(p.s, b);
+  if (sq.tiles == 0) return;
+  // where the unit's tiles lie in the list of all tiles
+  long long total = 0, before = 0;
+  for (int b0 = 0; b0 < p.s.B; b0 += 32) {
+    long long n = 0;
+    if (b0 + lane < p.s.B) n = span::seq_of(p.s, b0 + lane).tiles * upt;
+    long long nb = b0 + lane < b ? n : 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      n += __shfl_xor_sync(0xffffffffu, n, o);
+      nb += __shfl_xor_sync(0xffffffffu, nb, o);
+    }
+    total += n;
+    before += nb;
+  }
+  const long long per = max(1LL, (total + grid_tc - 1) / grid_tc);
+  const long long u0 = before + in_seq * sq.tiles, u1 = u0 + sq.tiles;
+  const long long c0 = u0 / per, c1 = (u1 - 1) / per;
+  const int g = (int)(in_seq % p.s.Hkv), r0 = (int)(in_seq / p.s.Hkv) * rows_per_unit;
+  const int half = blockIdx.z;  // pair: which of the two row tiles
+  const int m = threadIdx.x % kTcTile, q4 = (int)blockIdx.y * kMergeCols + threadIdx.x / kTcTile;
+  const int row = r0 + half * kTcTile + m;
+  if (row >= p.s.R || row % p.s.T >= sq.n_b) return;
+  const int n_str = p.pair ? 1 : 2;  // partials of a row in one run
+  auto part = [&](long long c, int w) { return p.s.part + ((size_t)(unit + c) * 2 + (p.pair ? half : w)) * kPartFloats; };
+  float M = -INFINITY;
+  for (long long c = c0; c <= c1; ++c)
+    for (int w = 0; w < n_str; ++w) M = fmaxf(M, __ldcg(part(c, w) + m));
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (long long c = c0; c <= c1; ++c)
+    for (int w = 0; w < n_str; ++w) {
+      const float* pp = part(c, w);
+      const float mc = __ldcg(pp + m);
+      if (mc == -INFINITY) continue;  // nothing seen in this run (or the stream had no tile: O was not written)
+      const float f = exp2f(mc - M);
+      l = fmaf(__ldcg(pp + kTcTile + m), f, l);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + 2 * kTcTile) + (size_t)q4 * kTcTile + m);
+      o.x = fmaf(v.x, f, o.x);
+      o.y = fmaf(v.y, f, o.y);
+      o.z = fmaf(v.z, f, o.z);
+      o.w = fmaf(v.w, f, o.w);
+    }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.s.out) +
+                       (((size_t)b * p.s.Hq + (size_t)g * p.s.G) * p.s.T + row) * kHeadDim + 4 * q4;
+  *reinterpret_cast<uint2*>(out) = make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
+}
+
+template <bool TREE, bool PAGED>
+cudaError_t configure_tc() {
+  static std::mutex mu;
+  static std::map<int, cudaError_t> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  auto it = done.find(dev);
+  if (it != done.end()) return it->second;
+  e = cudaFuncSetAttribute(span_tc_kernel<TREE, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  done[dev] = e;
+  return e;
+}
+
+}  // namespace
+
+size_t span_tc_part_bytes(const hata_dims_t& d, int n_tok) {
+  const long long R = (long long)(d.n_q_heads / d.n_kv_heads) * n_tok;
+  const long long rows = R > kTcTile ? 2 * kTcTile : kTcTile;
+  const size_t units = (size_t)d.batch * d.n_kv_heads * (size_t)((R + rows - 1) / rows);
+  return (units + (size_t)span_sms()) * 2 * kPartFloats * 4;
+}
+
+cudaError_t launch_span_tc(const hata_dims_t& d, const span::Params& s, const PagedCache* pg, cudaStream_t st) {
+  const int sms = span_sms();
+  TcParams p{};
+  p.s = s;
+  p.pair = s.R > kTcTile ? 1 : 0;
+  const int rows = p.pair ? 2 * kTcTile : kTcTile;
+  p.s.row_tiles = (s.R + rows - 1) / rows;
+  p.test_expire = (d.flags & HATA_FLAG_TEST_EXPIRE_WAIT) ? 1 : 0;
+  CUtensorMap qm, km, vm;
+  p.box_rows = pg ? std::min(1 << pg->block_shift, kTcTile) : kTcTile;
+  const long long kv_rows =
+      pg ? ((long long)pg->n_blocks * d.n_kv_heads) << pg->block_shift : (long long)d.batch * d.n_kv_heads * d.max_seq;
+  const long long q_rows = (long long)d.batch * d.n_q_heads * s.T;
+  if (kv_rows + kTcTile > 0x7fffffffLL || q_rows + 2 * kTcTile > 0x7fffffffLL) return cudaErrorNotSupported;
+  if (!make_bf16_rows_map(&qm, s.q, q_rows, kTcTile) || !make_bf16_rows_map(&km, s.K, kv_rows, p.box_rows) ||
+      !make_bf16_rows_map(&vm, s.V, kv_rows, p.box_rows))
+    return cudaErrorNotSupported;
+  cudaError_t e = pg ? configure_tc<true, true>() : configure_tc<true, false>();
+  if (e != cudaSuccess) return e;
+  if (pg) span_tc_kernel<true, true><<<sms, kTcThreads, kTcSmem, st>>>(qm, km, vm, p);
+  else span_tc_kernel<true, false><<<sms, kTcThreads, kTcSmem, st>>>(qm, km, vm, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const long long units = (long long)d.batch * d.n_kv_heads * p.s.row_tiles;
+  if (units > 0x7fffffffLL) return cudaErrorNotSupported;
+  span_merge_kernel<<<dim3((unsigned)units, kHeadDim / 4 / kMergeCols, p.pair ? 2 : 1), kTcTile * kMergeCols, 0, st>>>(
+      p, sms, rows);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_window_prefill(const hata_dims_t& d, const void* q, const void* K, const void* V,
+                                  const int32_t* seq_lens, int window, int sink, float scale, void* out,
+                                  uint32_t* status, cudaStream_t st) {
+  TcParams p{};
+  p.s.q = q;
+  p.s.K = K;
+  p.s.V = V;
+  p.s.out = out;
+  p.s.status = status;
+  p.s.seq_lens = seq_lens;
+  p.s.B = d.batch;
+  p.s.Hq = d.n_q_heads;
+  p.s.Hkv = d.n_kv_heads;
+  p.s.G = d.n_q_heads / d.n_kv_heads;
+  p.s.max_seq = d.max_seq;
+  p.s.window = window;
+  p.s.sink = sink;
+  p.s.scale_log2 = scale * 1.4426950408889634f;
+  p.test_expire = (d.flags & HATA_FLAG_TEST_EXPIRE_WAIT) ? 1 : 0;
+  p.prefill_heads = p.s.G & -p.s.G;  // a power of two, at most 16 (G <= 16)
+  p.pos_block = 2 * kTcTile / p.prefill_heads;
+  p.q_box = std::min(p.pos_block, kTcTile);
+  p.n_blocks_pos = (d.max_seq + p.pos_block - 1) / p.pos_block;
+  p.box_rows = kTcTile;
+  const long long q_rows = (long long)d.batch * d.n_q_heads * d.max_seq, kv_rows = (long long)d.batch * d.n_kv_heads * d.max_seq;
+  if (q_rows + 2 * kTcTile > 0x7fffffffLL) return cudaErrorNotSupported;
+  CUtensorMap qm, km, vm;
+  if (!make_bf16_rows_map(&qm, q, q_rows, p.q_box) || !make_bf16_rows_map(&km, K, kv_rows, kTcTile) ||
+      !make_bf16_rows_map(&vm, V, kv_rows, kTcTile))
+    return cudaErrorNotSupported;
+  cudaError_t e = configure_tc<false, false>();
+  if (e != cudaSuccess) return e;
+  const long long items = (long long)p.n_blocks_pos * d.batch * (d.n_q_heads / p.prefill_heads);
+  const unsigned grid = (unsigned)std::min<long long>(items, span_sms());
+  span_tc_kernel<false, false><<<grid, kTcThreads, kTcSmem, st>>>(qm, km, vm, p);
+  return cudaGetLastError();
+}
+
+}  // namespace hata

@@ -405,6 +405,20 @@ HATA_API hata_status_t hata_window_decode_paged(const hata_dims_t* dims, const v
                                                 void* stream);
 
 /*
+ * Causal prefill attention with a sliding window and sinks: position t < L_b = seq_lens[b] sees s
+ * iff s <= t and (s < n_sink or s > t - window):
+ *     out[b][h][t] = sum_s softmax_s(scale * q[b][h][t] . K[b][g][s]) V[b][g][s]
+ * Layouts, types (bf16) and rounding of hata_prefill_attention; rows t >= L_b of out are
+ * not written, and rows of K and V at or past L_b may hold anything.  window >= 1,
+ * n_sink >= 0; scale <= 0 selects 1/sqrt(d).  L_b > max_seq is clamped and flagged; a
+ * bounded wait that runs out records HATA_ERR_TIMEOUT.  The workspace is at least
+ * 16 bytes: its status word.  (The keys' codes: hata_encode_append.)
+ */
+HATA_API hata_status_t hata_window_prefill(const hata_dims_t* dims, const void* q, const void* K, const void* V,
+                                           const int32_t* seq_lens, int window, int n_sink, float scale, void* out,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Attention of n_tok drafted tokens per sequence over a cache that already holds them
  * (hata_norm_rope wrote them): the verification of speculative decoding.  With
  * L_b = seq_lens[b] including them, n_b = n_new[b] of them (NULL: n_tok) and
