@@ -127,13 +127,7 @@ __device__ __forceinline__ Cursor find(const Params& p, long long at, int lane) 
   return c;
 }
 
-// Whether any row of the call sees slot s of the sequence.
-__device__ __forceinline__ bool in_span(const Params& p, const Seq& q, int s) {
-  if (s >= q.L) return false;
-  return p.window <= 0 || s < p.sink || s >= q.L - p.window;
-}
-
-// Whether row r (query head r / T of the group, new token r % T) sees slot s; in_span(s) holds.
+// Whether new token i sees slot s, a slot that some token may see.
 __device__ __forceinline__ bool sees(const Params& p, const Seq& q, int b, int i, int s) {
   const int j = s - q.ctx;
   if (j < 0) return true;
@@ -141,28 +135,22 @@ __device__ __forceinline__ bool sees(const Params& p, const Seq& q, int b, int i
   return (p.mask[((size_t)b * p.T + i) * p.mask_words + (j >> 5)] >> (j & 31)) & 1u;
 }
 
+// The n lowest bits (none below 1, all from 32 on).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
 // A slot that no token sees may hold anything (a value row that is not finite would turn 0 * V into NaN), so
 // it is read as zeros.  Bit k of the answer: some token sees slot s0 + k (k < 16).  All lanes of a warp.
 __device__ __forceinline__ unsigned seen_by_any16(const Params& p, const Seq& q, int b, int s0, int lane) {
-  unsigned in = 0;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) in |= in_span(p, q, s0 + k) ? 1u << k : 0u;
-  if (s0 + 16 <= q.ctx || !p.mask) return in;
+  unsigned in = low_bits(min(16, q.L - s0));
+  if (p.window > 0) in &= low_bits(p.sink - s0) | ~low_bits(q.L - min(p.window, q.L) - s0);
+  if (s0 + 16 <= q.ctx || !p.mask || !in) return in;
   unsigned any = 0;
   for (int i = lane; i < q.n_b; i += 32)
     for (int k = max(0, q.ctx - s0); k < 16; ++k)
       if ((in >> k) & 1u) any |= sees(p, q, b, i, s0 + k) ? 1u << k : 0u;
   any = __reduce_or_sync(0xffffffffu, any);
-  const int c = q.ctx - s0;  // slots before the new tokens are seen by all
-  return in & (any | (c > 0 ? (1u << c) - 1u : 0u));
+  return in & (any | low_bits(q.ctx - s0));  // slots before the new tokens are seen by all
 }
-
-template <typename T>
-__device__ __forceinline__ void store_out(T* out, float v);
-template <>
-__device__ __forceinline__ void store_out<float>(float* out, float v) { *out = v; }
-template <>
-__device__ __forceinline__ void store_out<__nv_bfloat16>(__nv_bfloat16* out, float v) { *out = __float2bfloat16_rn(v); }
 
 }  // namespace span
 

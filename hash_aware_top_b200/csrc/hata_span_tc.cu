@@ -174,7 +174,6 @@ struct Bits128 {
     return __funnelshift_r(word(i), word(i + 1), j0 & 31);
   }
 };
-__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
 template <bool TREE, bool PAGED>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -412,15 +411,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (p.s.mask_words > 2) seen.w2 = mw[2];
             if (p.s.mask_words > 3) seen.w3 = mw[3];
           } else {
-            seen.w0 = below(i + 1);
-            seen.w1 = below(i - 31);
-            seen.w2 = below(i - 63);
-            seen.w3 = below(i - 95);
+            seen.w0 = span::low_bits(i + 1);
+            seen.w1 = span::low_bits(i - 31);
+            seen.w2 = span::low_bits(i - 63);
+            seen.w3 = span::low_bits(i - 95);
           }
-          seen.w0 &= below(sg.n_b);
-          seen.w1 &= below(sg.n_b - 32);
-          seen.w2 &= below(sg.n_b - 64);
-          seen.w3 &= below(sg.n_b - 96);
+          seen.w0 &= span::low_bits(sg.n_b);
+          seen.w1 &= span::low_bits(sg.n_b - 32);
+          seen.w2 &= span::low_bits(sg.n_b - 64);
+          seen.w3 &= span::low_bits(sg.n_b - 96);
           // the new tokens that any token sees
           any = {0u, 0u, 0u, 0u};
           for (int j = lane; p.s.mask && j < sg.n_b; j += 32) {
@@ -430,10 +429,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (p.s.mask_words > 2) any.w2 |= mw[2];
             if (p.s.mask_words > 3) any.w3 |= mw[3];
           }
-          any.w0 = __reduce_or_sync(0xffffffffu, p.s.mask ? any.w0 : 0xffffffffu) & below(sg.n_b);
-          any.w1 = __reduce_or_sync(0xffffffffu, p.s.mask ? any.w1 : 0xffffffffu) & below(sg.n_b - 32);
-          any.w2 = __reduce_or_sync(0xffffffffu, p.s.mask ? any.w2 : 0xffffffffu) & below(sg.n_b - 64);
-          any.w3 = __reduce_or_sync(0xffffffffu, p.s.mask ? any.w3 : 0xffffffffu) & below(sg.n_b - 96);
+          any.w0 = __reduce_or_sync(0xffffffffu, p.s.mask ? any.w0 : 0xffffffffu) & span::low_bits(sg.n_b);
+          any.w1 = __reduce_or_sync(0xffffffffu, p.s.mask ? any.w1 : 0xffffffffu) & span::low_bits(sg.n_b - 32);
+          any.w2 = __reduce_or_sync(0xffffffffu, p.s.mask ? any.w2 : 0xffffffffu) & span::low_bits(sg.n_b - 64);
+          any.w3 = __reduce_or_sync(0xffffffffu, p.s.mask ? any.w3 : 0xffffffffu) & span::low_bits(sg.n_b - 96);
         }
       } else {
         t = p.prefill_heads == 1 ? sg.row0 + w * kTcTile + m : sg.row0 + m % p.pos_block;
