@@ -33,10 +33,17 @@ constexpr float kSpSlack = 8.f;  // log2 units
 static_assert(kSpWarps * kSpKeys == kSpanTile, "the warps share a tile");
 
 // 16-byte copy, or 16 zero bytes where !valid
-__device__ __forceinline__ void cp_async16_zfill(void* smem, const void* gmem, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(ptx::smem_u32(smem)), "l"(gmem),
-               "r"(valid ? 16 : 0)
+__device__ __forceinline__ void cp_async16_zfill(uint32_t smem, const void* gmem, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem), "l"(gmem), "r"(valid ? 16 : 0)
                : "memory");
+}
+__device__ __forceinline__ void cp_async16_at(uint32_t smem, const void* gmem) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // First cache row of 16 consecutive slots from s0 (a multiple of 16, below L): in one page, since pages
@@ -66,7 +73,7 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* out, float4
       make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
 }
 
-// The weights that bring n partials of each row to one maximum: sm_m, sm_l [n][ROWS] (maximum, sum) become
+// The weights that bring the warps' outputs of each row to one maximum: sm_m, sm_l [n][ROWS] (maximum, sum) become
 // sm_m = 2^(m - M) and, for row r, (M, sum of l 2^(m - M)) in row_m, row_l.  A warp per row; all threads.
 template <int ROWS>
 __device__ __forceinline__ void join_weights(float* sm_m, const float* sm_l, int n, float* row_m, float* row_l) {
@@ -93,84 +100,107 @@ __device__ __forceinline__ void join_weights(float* sm_m, const float* sm_l, int
   __syncthreads();
 }
 
-// The end of a unit's run in this CTA.  In shared memory: m, l [kSpWarps][ROWS] and o [kSpWarps][ROWS][128]
-// of the warps.  Joins them, then writes the rows, or leaves a partial and, as the last to arrive, joins
-// the partials.  `scratch`: 2 * gridDim.x * ROWS floats for the latter (over o).  All threads of the CTA.
+constexpr int kOutRow = kHeadDim + 8;  // floats of a row of a warp's output in shared memory: rows on distinct banks
+
+// A partial: m [ROWS], l [ROWS], O [ROWS][128].  A CTA continues one unit at most (slot 0) and leaves one at most (1).
+template <int ROWS>
+__device__ __forceinline__ float* part_of(const Params& p, long long cta, long long per, long long u0) {
+  return p.part + ((size_t)cta * 2 + (cta * per > u0 ? 0 : 1)) * ROWS * (kHeadDim + 2);
+}
+
+// The end of a unit's run in this CTA.  In shared memory: m, l [kSpWarps][ROWS] and o [kSpWarps][ROWS][kOutRow]
+// of the warps.  Joins them, then writes the rows of a unit that is all this CTA's, or leaves a partial.
 template <typename T, int ROWS>
-__device__ __forceinline__ void finish_unit(const Params& p, float* sm_m, float* sm_l, const float* sm_o, float* scratch,
-                                            int b, int n_b, int g, int rt, long long unit, long long u0, long long u1,
-                                            long long per, int cta) {
-  __shared__ int s_last;
+__device__ __forceinline__ void finish_unit(const Params& p, float* sm_m, float* sm_l, const float* sm_o, int b, int n_b,
+                                            int g, int rt, long long u0, long long u1, long long per) {
   __shared__ float row_m[ROWS], row_l[ROWS];
-  constexpr int kQuads = ROWS * kHeadDim / 4;
-  const int tid = threadIdx.x;
-  const long long c0 = u0 / per, c1 = (u1 - 1) / per;
-  const int r0 = rt * ROWS;
+  const int tid = threadIdx.x, r0 = rt * ROWS;
+  const bool whole = u0 / per == (u1 - 1) / per;
   T* out = static_cast<T*>(p.out) + (((size_t)b * p.Hq + (size_t)g * p.G) * p.T + r0) * kHeadDim;
-  auto live = [&](int r) { return r0 + r < p.R && (r0 + r) % p.T < n_b; };
-  const int slot = (long long)cta * per > u0 ? 0 : 1;  // a CTA continues one unit at most, and leaves one at most
-  float* part = p.part + ((size_t)cta * 2 + slot) * ROWS * (kHeadDim + 2);
+  float* part = part_of<ROWS>(p, blockIdx.x, per, u0);
   join_weights<ROWS>(sm_m, sm_l, kSpWarps, row_m, row_l);
-  for (int e = tid; e < kQuads; e += kSpThreads) {
-    const int r = e / (kHeadDim / 4);
+  for (int e = tid; e < ROWS * kHeadDim / 4; e += kSpThreads) {
+    const int r = e / (kHeadDim / 4), c = e % (kHeadDim / 4);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kSpWarps; ++w) {
       const float f = sm_m[w * ROWS + r];
-      const float4 v = reinterpret_cast<const float4*>(sm_o)[w * kQuads + e];
+      const float4 v = *reinterpret_cast<const float4*>(sm_o + (w * ROWS + r) * kOutRow + 4 * c);
       o.x = fmaf(v.x, f, o.x);
       o.y = fmaf(v.y, f, o.y);
       o.z = fmaf(v.z, f, o.z);
       o.w = fmaf(v.w, f, o.w);
     }
-    if (c0 == c1) {
+    if (whole) {
       const float l = row_l[r], inv = l == 0.f ? 0.f : 1.f / l;
-      if (live(r)) store4<T>(out + 4 * e, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+      if (r0 + r < p.R && (r0 + r) % p.T < n_b)
+        store4<T>(out + 4 * e, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     } else {
       reinterpret_cast<float4*>(part + 2 * ROWS)[e] = o;
     }
   }
-  if (c0 == c1) return;
-  if (tid < ROWS) {
+  if (!whole && tid < ROWS) {
     part[tid] = row_m[tid];
     part[ROWS + tid] = row_l[tid];
   }
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) s_last = atomicAdd(&p.count[unit], 1u) == (unsigned)(c1 - c0);
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  const int n = (int)(c1 - c0) + 1;  // at most gridDim.x
-  auto part_of = [&](int i) {
-    const long long c = c0 + i;
-    return p.part + ((size_t)c * 2 + (c * per > u0 ? 0 : 1)) * ROWS * (kHeadDim + 2);
-  };
-  float *wm = scratch, *wl = scratch + n * ROWS;
-  for (int e = tid; e < n * ROWS; e += kSpThreads) {
-    const float* pp = part_of(e / ROWS) + e % ROWS;
-    wm[e] = __ldcg(pp);
-    wl[e] = __ldcg(pp + ROWS);
-  }
-  __syncthreads();
-  join_weights<ROWS>(wm, wl, n, row_m, row_l);
-  for (int e = tid; e < kQuads; e += kSpThreads) {
-    const int r = e / (kHeadDim / 4);
-    if (!live(r)) continue;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float f = wm[i * ROWS + r];
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of(i) + 2 * ROWS) + e);
-      o.x = fmaf(v.x, f, o.x);
-      o.y = fmaf(v.y, f, o.y);
-      o.z = fmaf(v.z, f, o.z);
-      o.w = fmaf(v.w, f, o.w);
+}
+
+// Joins the partials of a unit in the order of the split: a warp per row, a lane per 4 columns.
+// grid = (units, ROWS / 4).
+constexpr int kJoinWarps = 4;
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(kJoinWarps * 32) span_join_kernel(const Params p, int grid_main) {
+  const int lane = threadIdx.x & 31, r = (int)blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  const long long upt = (long long)p.Hkv * p.row_tiles, unit = blockIdx.x, in_seq = unit % upt;
+  const int b = (int)(unit / upt), g = (int)(in_seq % p.Hkv), row = (int)(in_seq / p.Hkv) * ROWS + r;
+  ptx::pdl_wait();
+  const Seq sq = seq_of(p, b);
+  if (sq.tiles == 0 || row >= p.R || row % p.T >= sq.n_b) return;
+  long long total, before;
+  count_tiles(p, lane, b, false, &total, &before);
+  const long long per = max(1LL, (total + grid_main - 1) / grid_main);
+  const long long u0 = before + in_seq * sq.tiles, c0 = u0 / per, c1 = (u0 + sq.tiles - 1) / per;
+  if (c0 == c1) return;  // written by the one CTA that had it
+  const int n = (int)(c1 - c0) + 1;
+  float M = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += 32) {  // 32 runs: a lane per run for the weights, then a lane per column for O
+    float m = -INFINITY, li = 0.f;
+    if (i0 + lane < n) {
+      const float* pp = part_of<ROWS>(p, c0 + i0 + lane, per, u0);
+      m = __ldcg(pp + r);
+      li = __ldcg(pp + ROWS + r);
     }
-    const float l = row_l[r], inv = l == 0.f ? 0.f : 1.f / l;
-    store4<T>(out + 4 * e, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    float mx = m;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+    const float m_new = fmaxf(M, mx);
+    const float back = m_new == -INFINITY ? 1.f : exp2f(M - m_new);
+    const float f = m == -INFINITY ? 0.f : exp2f(m - m_new);
+    float ls = li * f;
+#pragma unroll
+    for (int k = 16; k; k >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, k);
+    l = fmaf(l, back, ls);
+    o.x *= back;
+    o.y *= back;
+    o.z *= back;
+    o.w *= back;
+    M = m_new;
+    const int k1 = min(32, n - i0);
+#pragma unroll 8
+    for (int k = 0; k < k1; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of<ROWS>(p, c0 + i0 + k, per, u0) + 2 * ROWS) +
+                              r * (kHeadDim / 4) + lane);
+      o.x = fmaf(v.x, fk, o.x);
+      o.y = fmaf(v.y, fk, o.y);
+      o.z = fmaf(v.z, fk, o.z);
+      o.w = fmaf(v.w, fk, o.w);
+    }
   }
-  if (tid == 0) p.count[unit] = 0u;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* out = static_cast<T*>(p.out) + (((size_t)b * p.Hq + (size_t)g * p.G) * p.T + row) * kHeadDim + 4 * lane;
+  store4<T>(out, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
 
 __device__ __forceinline__ float4 load4(const unsigned char* row, int d) {
@@ -181,8 +211,8 @@ template <int ROWS>
 struct SimtSmem {
   static constexpr int kRowB = kHeadDim * 4 + 16;  // padded: 16 rows on distinct banks
   static constexpr int kWarpB = 2 * kSpKeys * kRowB;            // K then V of a warp's slots
-  static constexpr int kStage = kSpWarps * kWarpB > kSpWarps * ROWS * kHeadDim * 4 ? kSpWarps * kWarpB
-                                                                                   : kSpWarps * ROWS * kHeadDim * 4;
+  static constexpr int kStage = kSpWarps * kWarpB;              // later o [warps][ROWS][kOutRow] fp32
+  static_assert(ROWS * kOutRow * 4 <= kWarpB, "the warps' outputs lie over their staged rows");
   static constexpr int kQ = kStage;                               // [ROWS][128] fp32
   static constexpr int kP = kQ + ROWS * kHeadDim * 4;             // [warps][ROWS][16] fp32
   static constexpr int kML = kP + kSpWarps * ROWS * kSpKeys * 4;  // m, l [warps][ROWS]
@@ -191,7 +221,7 @@ struct SimtSmem {
 
 template <int ROWS, bool PAGED>
 __global__ void __launch_bounds__(kSpThreads, 1) span_simt_kernel(const Params p) {
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ __align__(1024) unsigned char smem[];
   using S = SimtSmem<ROWS>;
   using T = float;
   float* sm_q = reinterpret_cast<float*>(smem + S::kQ);
@@ -203,12 +233,10 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_simt_kernel(const Params p
   unsigned char* vt = kt + kSpKeys * S::kRowB;
   float* sm_p = reinterpret_cast<float*>(smem + S::kP) + warp * ROWS * kSpKeys;
 
-  const long long total = total_tiles(p, lane, blockIdx.x == 0 && warp == 0);
-  const long long per = max(1LL, (total + gridDim.x - 1) / gridDim.x);
-  long long at = (long long)blockIdx.x * per;
-  const long long end = min(total, at + per);
-  if (at >= end) return;
-  Cursor cur = find(p, at, lane);
+  ptx::pdl_launch_dependents();  // the joining kernel may be set up; it waits for this one to end
+  long long at, end, per;
+  Cursor cur;
+  if (!my_run(p, lane, blockIdx.x == 0 && warp == 0, &at, &end, &per, &cur)) return;
   const int key = lane & 15, half = lane >> 4;
   while (at < end) {
     while (at >= cur.seq_start + (long long)cur.seq.tiles * p.Hkv * p.row_tiles) {
@@ -249,8 +277,8 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_simt_kernel(const Params p
         const int k = e / VPR, c = e % VPR;
         const bool ok = (vis >> k) & 1u;
         const size_t off = ok ? (size_t)k * kHeadDim * sizeof(T) + c * 16 : 0;
-        cp_async16_zfill(kt + k * S::kRowB + c * 16, Kg + off, ok);
-        cp_async16_zfill(vt + k * S::kRowB + c * 16, Vg + off, ok);
+        cp_async16_zfill(ptx::smem_u32(kt) + k * S::kRowB + c * 16, Kg + off, ok);
+        cp_async16_zfill(ptx::smem_u32(vt) + k * S::kRowB + c * 16, Vg + off, ok);
       }
       ptx::cp_async_wait_all();
       __syncwarp();
@@ -314,12 +342,11 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_simt_kernel(const Params p
         sm_m[warp * ROWS + r] = m[r];
         sm_l[warp * ROWS + r] = l[r];
       }
-      *reinterpret_cast<float4*>(sm_o + ((size_t)warp * ROWS + r) * kHeadDim + 4 * lane) =
+      *reinterpret_cast<float4*>(sm_o + (warp * ROWS + r) * kOutRow + 4 * lane) =
           make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
     }
     __syncthreads();
-    long long unit = (long long)b * p.Hkv * p.row_tiles + in_seq;
-    finish_unit<T, ROWS>(p, sm_m, sm_l, sm_o, sm_o, b, sq.n_b, g, rt, unit, u0, u1, per, (int)blockIdx.x);
+    finish_unit<T, ROWS>(p, sm_m, sm_l, sm_o, b, sq.n_b, g, rt, u0, u1, per);
     __syncthreads();
     at = u0 + j1;
   }
@@ -335,10 +362,11 @@ constexpr int kMmWarpB = kMmStages * kMmStageB;
 template <int MT>
 struct MmaSmem {
   static constexpr int kRows = 16 * MT;
-  static constexpr int kStage = kSpWarps * kMmWarpB;  // later o [warps][rows][128] fp32: 64 KB per 16 rows
-  static constexpr int kML = kStage;                  // m, l [warps][rows]
+  static constexpr int kStage = kSpWarps * kMmWarpB;  // later o [warps][rows][kOutRow] fp32
+  static constexpr int kQ = kStage;                   // query rows, pieces placed as those of K
+  static constexpr int kML = kQ + kRows * kMmRowB;    // m, l [warps][rows]
   static constexpr int kBytes = kML + 2 * kSpWarps * kRows * 4;
-  static_assert(kSpWarps * kRows * kHeadDim * 4 <= kStage, "the warps' outputs lie over their stages");
+  static_assert(kRows * kOutRow * 4 <= kMmWarpB, "the warps' outputs lie over their stages");
 };
 
 __device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
@@ -366,22 +394,28 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 template <int MT, bool PAGED>
 __global__ void __launch_bounds__(kSpThreads, 1) span_mma_kernel(const Params p) {
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ __align__(1024) unsigned char smem[];
   using S = MmaSmem<MT>;
   constexpr int ROWS = S::kRows;
   float* sm_m = reinterpret_cast<float*>(smem + S::kML);
   float* sm_l = sm_m + kSpWarps * ROWS;
   float* sm_o = reinterpret_cast<float*>(smem);
+  const uint32_t sm_q = ptx::smem_u32(smem) + S::kQ;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gq = lane >> 2, cq = lane & 3;
-  unsigned char* stages = smem + warp * kMmWarpB;
-  const uint32_t stages_u = ptx::smem_u32(stages);
+  const uint32_t stages_u = ptx::smem_u32(smem) + (uint32_t)(warp * kMmWarpB);
+  uint32_t to[4];  // where copy e goes, less 512 e
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    to[i] = (uint32_t)((lane >> 4) * kMmRowB + (((lane & 15) ^ ((2 * i + (lane >> 4)) & 7)) << 4));
+  // this lane's row of the fragments: piece 0 of K (slots 0-7 and 8-15, low and high 8 dimensions) and of V
+  const int kkey = ((lane >> 4) << 3) + (lane & 7), vkey = (((lane >> 3) & 1) << 3) + (lane & 7);
+  const uint32_t kfrag = (uint32_t)(kkey * kMmRowB + ((((lane >> 3) & 1) ^ (kkey & 7)) << 4));
+  const uint32_t vfrag = (uint32_t)(vkey * kMmRowB + (((lane >> 4) ^ (vkey & 7)) << 4)) + kSpKeys * kMmRowB;
 
-  const long long total = total_tiles(p, lane, blockIdx.x == 0 && warp == 0);
-  const long long per = max(1LL, (total + gridDim.x - 1) / gridDim.x);
-  long long at = (long long)blockIdx.x * per;
-  const long long end = min(total, at + per);
-  if (at >= end) return;
-  Cursor cur = find(p, at, lane);
+  ptx::pdl_launch_dependents();  // the joining kernel may be set up; it waits for this one to end
+  long long at, end, per;
+  Cursor cur;
+  if (!my_run(p, lane, blockIdx.x == 0 && warp == 0, &at, &end, &per, &cur)) return;
   while (at < end) {
     while (at >= cur.seq_start + (long long)cur.seq.tiles * p.Hkv * p.row_tiles) {
       cur.seq_start += (long long)cur.seq.tiles * p.Hkv * p.row_tiles;
@@ -406,39 +440,51 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_mma_kernel(const Params p)
           const size_t row = rows_of16<PAGED>(p, b, g, s0);
           const unsigned char* Kg = static_cast<const unsigned char*>(p.K) + row * kMmRowB;
           const unsigned char* Vg = static_cast<const unsigned char*>(p.V) + row * kMmRowB;
-          unsigned char* st = stages + (j % kMmStages) * kMmStageB;
+          const uint32_t st = stages_u + (uint32_t)((j % kMmStages) * kMmStageB);
+          // copy e: row 2 e + lane / 16, piece lane % 16
+          if (vis == 0xffffu) {
+            const unsigned char *Kl = Kg + lane * 16, *Vl = Vg + lane * 16;
 #pragma unroll
-          for (int e = 0; e < kSpKeys * 16 / 32; ++e) {
-            const int k = 2 * e + (lane >> 4), c = lane & 15;
-            const bool ok = (vis >> k) & 1u;
-            const int off = ok ? k * kMmRowB + c * 16 : 0;
-            const int to = k * kMmRowB + ((c ^ (k & 7)) << 4);
-            cp_async16_zfill(st + to, Kg + off, ok);
-            cp_async16_zfill(st + kSpKeys * kMmRowB + to, Vg + off, ok);
+            for (int e = 0; e < kSpKeys / 2; ++e) {
+              cp_async16_at(st + to[e & 3] + 512 * e, Kl + 512 * e);
+              cp_async16_at(st + to[e & 3] + 512 * e + kSpKeys * kMmRowB, Vl + 512 * e);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < kSpKeys / 2; ++e) {
+              const bool ok = (vis >> (2 * e + (lane >> 4))) & 1u;
+              const int off = ok ? lane * 16 + 512 * e : 0;
+              cp_async16_zfill(st + to[e & 3] + 512 * e, Kg + off, ok);
+              cp_async16_zfill(st + to[e & 3] + 512 * e + kSpKeys * kMmRowB, Vg + off, ok);
+            }
           }
         }
       }
       asm volatile("cp.async.commit_group;\n" ::: "memory");
     };
-#pragma unroll
-    for (int k = 0; k < kMmStages - 1; ++k) load(j0 + k);
-    // query fragments of the unit's rows (zeros past the last)
-    uint32_t qa[MT][kHeadDim / 16][4];
+    // query rows of the unit (zeros past the last), the first group of copies
     {
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
-                               (((size_t)b * p.Hq + (size_t)g * p.G) * p.T + r0) * kHeadDim + 2 * cq;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int ks = 0; ks < kHeadDim / 16; ++ks)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int r = 16 * mt + gq + 8 * (k & 1);
-            qa[mt][ks][k] = r0 + r < p.R
-                                ? __ldg(reinterpret_cast<const uint32_t*>(q + (size_t)r * kHeadDim + 16 * ks + 8 * (k >> 1)))
-                                : 0u;
-          }
+                               (((size_t)b * p.Hq + (size_t)g * p.G) * p.T + r0) * kHeadDim;
+      for (int e = tid; e < ROWS * 16; e += kSpThreads) {
+        const int r = e >> 4, c = e & 15;
+        const bool ok = r0 + r < p.R;
+        cp_async16_zfill(sm_q + (uint32_t)(r * kMmRowB + ((c ^ (r & 7)) << 4)), q + (ok ? e * 8 : 0), ok);
+      }
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
     }
+#pragma unroll
+    for (int k = 0; k < kMmStages - 1; ++k) load(j0 + k);
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(kMmStages - 1) : "memory");
+    __syncthreads();
+    uint32_t qa[MT][kHeadDim / 16][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+        const int r = lane & 15, c = 2 * ks + (lane >> 4);
+        ldsm_x4(qa[mt][ks], sm_q + (uint32_t)((16 * mt + r) * kMmRowB + ((c ^ (r & 7)) << 4)));
+      }
     float o[MT][kHeadDim / 8][4];
     float m[MT][2], l[MT][2];
 #pragma unroll
@@ -458,7 +504,7 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_mma_kernel(const Params p)
       const int s0 = first_slot(j);
       const unsigned vis = seen_by_any16(p, sq, b, s0, lane);
       if (!vis) continue;  // nobody sees the warp's slots
-      const uint32_t kt = stages_u + (uint32_t)((j % kMmStages) * kMmStageB), vt = kt + kSpKeys * kMmRowB;
+      const uint32_t st = stages_u + (uint32_t)((j % kMmStages) * kMmStageB), kt = st + kfrag, vt = st + vfrag;
       float s[MT][2][4];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
@@ -466,17 +512,14 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_mma_kernel(const Params p)
         for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int k = 0; k < 4; ++k) s[mt][n][k] = 0.f;
-      {
-        const int key = ((lane >> 4) << 3) + (lane & 7), hi = (lane >> 3) & 1;
 #pragma unroll
-        for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-          uint32_t kb[4];  // slots 0-7: low and high 8 dimensions; slots 8-15: low and high
-          ldsm_x4(kb, kt + (uint32_t)(key * kMmRowB + (((2 * ks + hi) ^ (key & 7)) << 4)));
+      for (int ks = 0; ks < kHeadDim / 16; ++ks) {
+        uint32_t kb[4];  // slots 0-7: low and high 8 dimensions; slots 8-15: low and high
+        ldsm_x4(kb, kt ^ (uint32_t)(ks << 5));
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816(s[mt][0], qa[mt][ks], kb[0], kb[1]);
-            mma16816(s[mt][1], qa[mt][ks], kb[2], kb[3]);
-          }
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816(s[mt][0], qa[mt][ks], kb[0], kb[1]);
+          mma16816(s[mt][1], qa[mt][ks], kb[2], kb[3]);
         }
       }
       const bool all_see = vis == 0xffffu && s0 + kSpKeys <= sq.ctx;
@@ -491,7 +534,7 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_mma_kernel(const Params p)
           for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              float x = s[mt][n][2 * h + k] * p.scale_log2;
+              float x = s[mt][n][2 * h + k];
               if (!all_see) {
                 const int e = 8 * n + 2 * cq + k;
                 if (!((vis >> e) & 1u) || (s0 + e >= sq.ctx && !sees(p, sq, b, (r0 + 16 * mt + gq + 8 * h) % p.T, s0 + e)))
@@ -501,7 +544,7 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_mma_kernel(const Params p)
               mx = fmaxf(mx, x);
             }
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * p.scale_log2;  // the scale is positive
           x_max[mt][h] = mx;
           moves |= mx > m[mt][h] + kSpSlack;
         }
@@ -512,7 +555,7 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_mma_kernel(const Params p)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const float m_new = fmaxf(m[mt][h], x_max[mt][h]);
-            const float alpha = m_new == -INFINITY ? 1.f : exp2f(m[mt][h] - m_new);
+            const float alpha = m_new == -INFINITY ? 1.f : ex2(m[mt][h] - m_new);
             m[mt][h] = m_new;
             l[mt][h] *= alpha;
 #pragma unroll
@@ -530,24 +573,22 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_mma_kernel(const Params p)
           const float base = m[mt][h] == -INFINITY ? 0.f : m[mt][h];
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const __nv_bfloat162 pr = __floats2bfloat162_rn(exp2f(s[mt][n][2 * h] - base), exp2f(s[mt][n][2 * h + 1] - base));
+            const __nv_bfloat162 pr = __floats2bfloat162_rn(ex2(fmaf(s[mt][n][2 * h], p.scale_log2, -base)),
+                                                            ex2(fmaf(s[mt][n][2 * h + 1], p.scale_log2, -base)));
             const uint32_t u = *reinterpret_cast<const uint32_t*>(&pr);
             pa[mt][2 * n + h] = u;
             // the row sum takes p as P.V does, rounded: a row that one slot dominates comes out exact
             l[mt][h] += __uint_as_float(u << 16) + __uint_as_float(u & 0xffff0000u);
           }
         }
-      {
-        const int key = (((lane >> 3) & 1) << 3) + (lane & 7), hi = lane >> 4;
 #pragma unroll
-        for (int n = 0; n < kHeadDim / 16; ++n) {
-          uint32_t vb[4];  // dimensions 16 n .. + 7: slots 0-7, 8-15; then the next 8 dimensions
-          ldsm_x4_trans(vb, vt + (uint32_t)(key * kMmRowB + (((2 * n + hi) ^ (key & 7)) << 4)));
+      for (int n = 0; n < kHeadDim / 16; ++n) {
+        uint32_t vb[4];  // dimensions 16 n .. + 7: slots 0-7, 8-15; then the next 8 dimensions
+        ldsm_x4_trans(vb, vt ^ (uint32_t)(n << 5));
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816(o[mt][2 * n], pa[mt], vb[0], vb[1]);
-            mma16816(o[mt][2 * n + 1], pa[mt], vb[2], vb[3]);
-          }
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816(o[mt][2 * n], pa[mt], vb[0], vb[1]);
+          mma16816(o[mt][2 * n + 1], pa[mt], vb[2], vb[3]);
         }
       }
     }
@@ -567,12 +608,11 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_mma_kernel(const Params p)
         }
 #pragma unroll
         for (int n = 0; n < kHeadDim / 8; ++n)
-          *reinterpret_cast<float2*>(sm_o + ((size_t)warp * ROWS + r) * kHeadDim + 8 * n + 2 * cq) =
+          *reinterpret_cast<float2*>(sm_o + (warp * ROWS + r) * kOutRow + 8 * n + 2 * cq) =
               make_float2(o[mt][n][2 * h], o[mt][n][2 * h + 1]);
       }
     __syncthreads();
-    finish_unit<__nv_bfloat16, ROWS>(p, sm_m, sm_l, sm_o, sm_o, b, sq.n_b, g, rt,
-                                     (long long)b * p.Hkv * p.row_tiles + in_seq, u0, u1, per, (int)blockIdx.x);
+    finish_unit<__nv_bfloat16, ROWS>(p, sm_m, sm_l, sm_o, b, sq.n_b, g, rt, u0, u1, per);
     __syncthreads();
     at = u0 + j1;
   }
@@ -597,33 +637,33 @@ cudaError_t configure(Kernel k, int smem) {
   return e;
 }
 
-template <int ROWS, bool PAGED>
-cudaError_t launch_simt(Params p, cudaStream_t st) {
-  constexpr int smem = SimtSmem<ROWS>::kBytes;
-  cudaError_t e = configure(span_simt_kernel<ROWS, PAGED>, smem);
+template <typename T, int ROWS, typename Kernel>
+cudaError_t launch_rows(Kernel k, int smem, Params p, cudaStream_t st) {
+  cudaError_t e = configure(k, smem);
   if (e != cudaSuccess) return e;
   p.row_tiles = (p.R + ROWS - 1) / ROWS;
-  span_simt_kernel<ROWS, PAGED><<<span_sms(), kSpThreads, smem, st>>>(p);
-  return cudaGetLastError();
+  const long long units = (long long)p.B * p.Hkv * p.row_tiles;
+  if (units > 0x7fffffffLL) return cudaErrorNotSupported;
+  const int grid = span_sms();
+  k<<<grid, kSpThreads, smem, st>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_early(span_join_kernel<T, ROWS>, dim3((unsigned)units, ROWS / kJoinWarps), kJoinWarps * 32, st, p, grid);
 }
 
-template <int MT, bool PAGED>
-cudaError_t launch_mma(Params p, cudaStream_t st) {
-  constexpr int smem = MmaSmem<MT>::kBytes;
-  cudaError_t e = configure(span_mma_kernel<MT, PAGED>, smem);
-  if (e != cudaSuccess) return e;
-  p.row_tiles = (p.R + 16 * MT - 1) / (16 * MT);
-  span_mma_kernel<MT, PAGED><<<span_sms(), kSpThreads, smem, st>>>(p);
-  return cudaGetLastError();
+template <int ROWS>
+cudaError_t launch_simt(const Params& p, bool paged, cudaStream_t st) {
+  if (paged) return launch_rows<float, ROWS>(span_simt_kernel<ROWS, true>, SimtSmem<ROWS>::kBytes, p, st);
+  return launch_rows<float, ROWS>(span_simt_kernel<ROWS, false>, SimtSmem<ROWS>::kBytes, p, st);
 }
 
-// rows of the largest row tile, and of the smallest (most units)
-constexpr int kSpanMaxRows = 32, kSpanMinRows = 4;
-
-size_t count_bytes(const hata_dims_t& d, int n_tok) {
-  const size_t R = (size_t)(d.n_q_heads / d.n_kv_heads) * n_tok;
-  return align_up((size_t)d.batch * d.n_kv_heads * ((R + kSpanMinRows - 1) / kSpanMinRows) * 4, kAlign);
+template <int MT>
+cudaError_t launch_mma(const Params& p, bool paged, cudaStream_t st) {
+  if (paged) return launch_rows<__nv_bfloat16, 16 * MT>(span_mma_kernel<MT, true>, MmaSmem<MT>::kBytes, p, st);
+  return launch_rows<__nv_bfloat16, 16 * MT>(span_mma_kernel<MT, false>, MmaSmem<MT>::kBytes, p, st);
 }
+
+// rows of the largest row tile of the kernels here
+constexpr int kSpanMaxRows = 32;
 
 // bf16 with more rows per KV head than this runs on the tensor cores.
 constexpr int kSpanTcRows = 32;
@@ -655,8 +695,8 @@ int span_sms() {
 }
 
 size_t span_ws_bytes(const hata_dims_t& d, int n_tok) {
-  const size_t simt = (size_t)span_sms() * 2 * kSpanMaxRows * (kHeadDim + 2) * 4;
-  return kAlign + count_bytes(d, n_tok) + (use_tc(d, n_tok) ? std::max(simt, span_tc_part_bytes(d, n_tok)) : simt);
+  const size_t few = (size_t)span_sms() * 2 * kSpanMaxRows * (kHeadDim + 2) * 4;
+  return kAlign + (use_tc(d, n_tok) ? span_tc_part_bytes(d, n_tok) : few);
 }
 
 cudaError_t launch_span(const hata_dims_t& d, const SpanArgs& a, const PagedCache* pg, char* ws, cudaStream_t st) {
@@ -666,8 +706,7 @@ cudaError_t launch_span(const hata_dims_t& d, const SpanArgs& a, const PagedCach
   p.V = a.V;
   p.out = a.out;
   p.status = reinterpret_cast<uint32_t*>(ws);
-  p.count = reinterpret_cast<uint32_t*>(ws + kAlign);
-  p.part = reinterpret_cast<float*>(ws + kAlign + count_bytes(d, a.n_tok));
+  p.part = reinterpret_cast<float*>(ws + kAlign);
   p.seq_lens = a.seq_lens;
   p.n_new = a.n_new;
   p.mask = a.mask;
@@ -690,12 +729,8 @@ cudaError_t launch_span(const hata_dims_t& d, const SpanArgs& a, const PagedCach
   }
   if (a.window == 0 && use_tc(d, a.n_tok)) return launch_span_tc(d, p, pg, st);
   const bool paged = pg != nullptr;
-  if (d.dtype == HATA_BF16) {
-    if (p.R <= 16) return paged ? launch_mma<1, true>(p, st) : launch_mma<1, false>(p, st);
-    return paged ? launch_mma<2, true>(p, st) : launch_mma<2, false>(p, st);
-  }
-  if (p.R <= 4) return paged ? launch_simt<4, true>(p, st) : launch_simt<4, false>(p, st);
-  return paged ? launch_simt<16, true>(p, st) : launch_simt<16, false>(p, st);
+  if (d.dtype == HATA_BF16) return p.R <= 16 ? launch_mma<1>(p, paged, st) : launch_mma<2>(p, paged, st);
+  return p.R <= 4 ? launch_simt<4>(p, paged, st) : launch_simt<16>(p, paged, st);
 }
 
 }  // namespace hata

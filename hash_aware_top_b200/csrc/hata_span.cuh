@@ -1,5 +1,5 @@
 // Attention of a few query rows over a span of a cache, split over all SMs: what the kernels for
-// window decode and tree attention share (arguments, the split of the work, the merge of partials).
+// window decode and tree attention share (arguments, the split of the work).
 //
 // A unit is (sequence b, KV head g, tile of query rows).  The rows of a unit are the G * T (query
 // head of the group, new token) pairs, which lie next to each other in q and out.  Its keys are a
@@ -7,8 +7,9 @@
 // those that hold the window, for a window.  The tiles of all units, in the order (b, row tile, g, tile), are
 // cut into equal runs, one per CTA, so ragged lengths keep every SM busy to the end; a CTA's run may
 // end one unit and begin the next.  A unit that one CTA covers is written at once.  Otherwise each of
-// its CTAs leaves a partial (row maximum, row sum, weighted values; fp32) in the workspace and the last to
-// arrive merges them in the order of the split, so results do not depend on the order of arrival.
+// its CTAs leaves a partial (row maximum, row sum, weighted values; fp32) in the workspace, and a second kernel,
+// launched early (programmatic dependent launch), joins them in the order of the split.  Joining them in
+// the last CTA to arrive was slower: one SM then reads all partials of a unit (15 us for 32 rows and 19 runs).
 #pragma once
 
 #include "hata_kernels.cuh"
@@ -21,8 +22,7 @@ constexpr int kSpanTile = 128;  // cache slots of a tile
 struct Params {
   const void *q, *K, *V;
   void* out;
-  float* part;      // [grid][2][rows][kHeadDim + 2]
-  uint32_t* count;  // [units] arrivals, zero between calls
+  float* part;  // partials
   uint32_t* status;
   const int32_t *seq_lens, *n_new;
   const uint32_t* mask;  // [B][T][ceil(T / 32)], or null: token i sees tokens j <= i
@@ -76,16 +76,23 @@ __device__ __forceinline__ Seq seq_of(const Params& p, int b) {
 
 // Where a CTA stands in the list of tiles (the same in every thread of a warp).
 struct Cursor {
-  int b;                 // sequence
+  int b;                // sequence
   Seq seq;
-  long long seq_start;   // first tile of the sequence in the list of all tiles
+  long long seq_start;  // first tile of the sequence in the list of all tiles
 };
 
-// Number of tiles of all units, and the sequence that holds tile `at` of the list.  Every warp computes both
-// (32 sequences at a time), so no barrier is needed.
-__device__ __forceinline__ long long total_tiles(const Params& p, int lane, bool flag) {
-  long long sum = 0;
+__device__ __forceinline__ long long warp_sum(long long v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Tiles of all units, and of the units of sequences before b.  All lanes of a warp; every warp that needs them
+// computes them, 32 sequences at a time, so no barrier is needed.
+__device__ __forceinline__ void count_tiles(const Params& p, int lane, int b, bool flag, long long* total,
+                                            long long* before) {
   const long long per_tile = (long long)p.Hkv * p.row_tiles;
+  *total = *before = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     long long n = 0;
     if (b0 + lane < p.B) {
@@ -93,17 +100,23 @@ __device__ __forceinline__ long long total_tiles(const Params& p, int lane, bool
       n = s.tiles * per_tile;
       if (s.bad && flag) set_status(p.status, HATA_ERR_INVALID_ARG);
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    sum += n;
+    if (b0 < b) *before += warp_sum(b0 + lane < b ? n : 0);
+    *total += warp_sum(n);
   }
-  return sum;
 }
 
-__device__ __forceinline__ Cursor find(const Params& p, long long at, int lane) {
-  Cursor c;
-  c.b = 0;
-  c.seq_start = 0;
+// This CTA's run [*at, *end) of the list of all tiles, each CTA's length *per, and the sequence it begins in.
+// False: the CTA has none.
+__device__ __forceinline__ bool my_run(const Params& p, int lane, bool flag, long long* at, long long* end,
+                                       long long* per, Cursor* c) {
+  long long total, before;
+  count_tiles(p, lane, 0, flag, &total, &before);
+  *per = max(1LL, (total + gridDim.x - 1) / gridDim.x);
+  *at = (long long)blockIdx.x * *per;
+  *end = min(total, *at + *per);
+  if (*at >= *end) return false;
+  c->b = 0;
+  c->seq_start = 0;
   const long long per_tile = (long long)p.Hkv * p.row_tiles;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     long long n = 0;
@@ -114,17 +127,17 @@ __device__ __forceinline__ Cursor find(const Params& p, long long at, int lane) 
       const long long y = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += y;
     }
-    const unsigned past = __ballot_sync(0xffffffffu, c.seq_start + incl > at);
+    const unsigned past = __ballot_sync(0xffffffffu, c->seq_start + incl > *at);
     if (past) {
       const int l = __ffs(past) - 1;
-      c.b = b0 + l;
-      c.seq_start += __shfl_sync(0xffffffffu, incl - n, l);
+      c->b = b0 + l;
+      c->seq_start += __shfl_sync(0xffffffffu, incl - n, l);
       break;
     }
-    c.seq_start += __shfl_sync(0xffffffffu, incl, 31);
+    c->seq_start += __shfl_sync(0xffffffffu, incl, 31);
   }
-  c.seq = seq_of(p, c.b);
-  return c;
+  c->seq = seq_of(p, c->b);
+  return true;
 }
 
 // Whether new token i sees slot s, a slot that some token may see.
@@ -141,6 +154,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xfffffff
 // A slot that no token sees may hold anything (a value row that is not finite would turn 0 * V into NaN), so
 // it is read as zeros.  Bit k of the answer: some token sees slot s0 + k (k < 16).  All lanes of a warp.
 __device__ __forceinline__ unsigned seen_by_any16(const Params& p, const Seq& q, int b, int s0, int lane) {
+  if (p.window <= 0 && s0 + 16 <= q.ctx) return 0xffffu;
   unsigned in = low_bits(min(16, q.L - s0));
   if (p.window > 0) in &= low_bits(p.sink - s0) | ~low_bits(q.L - min(p.window, q.L) - s0);
   if (s0 + 16 <= q.ctx || !p.mask || !in) return in;
@@ -153,6 +167,22 @@ __device__ __forceinline__ unsigned seen_by_any16(const Params& p, const Seq& q,
 }
 
 }  // namespace span
+
+// Launches a kernel that may be set up while the one before it on the stream runs (and waits for it with
+// griddepcontrol.wait before it reads anything).
+template <typename... Args>
+cudaError_t launch_early(void (*k)(Args...), dim3 grid, unsigned threads, cudaStream_t st, Args... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
 
 // Tensor-core form of tree attention (hata_span_tc.cu): bf16, any number of rows.
 size_t span_tc_part_bytes(const hata_dims_t& d, int n_tok);

@@ -26,6 +26,7 @@
 #include <map>
 #include <mutex>
 
+#include "hata_ptx.cuh"
 #include "hata_span.cuh"
 #include "hata_tc.cuh"
 
@@ -91,11 +92,7 @@ struct Walk {
 
   __device__ __forceinline__ Walk(const TcParams& prm, int ln, bool flag) : p(prm), lane(ln) {
     if constexpr (TREE) {
-      const long long total = span::total_tiles(p.s, lane, flag);
-      per = max(1LL, (total + gridDim.x - 1) / gridDim.x);
-      at = (long long)blockIdx.x * per;
-      end = min(total, at + per);
-      if (at < end) cur = span::find(p.s, at, lane);
+      span::my_run(p.s, lane, flag, &at, &end, &per, &cur);
     } else {
       if (flag)
         for (int b = lane; b < p.s.B; b += 32)
@@ -231,6 +228,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   auto item_k = [&](int i, int w) { return pair ? 2 * i : 4 * i + w; };
   auto item_v = [&](int n, int i, int w) { return pair ? 2 * i + 1 : 4 * i + streams_in(n, i) + w; };
 
+  if constexpr (TREE) ptx::pdl_launch_dependents();  // the merge may be set up; it waits for this kernel to end
   Walk<TREE> walk(p, lane, blockIdx.x == 0 && warp == 0);
   Seg sg;
 
@@ -607,22 +605,12 @@ __global__ void __launch_bounds__(kTcTile* kMergeCols) span_merge_kernel(const T
   const long long unit = blockIdx.x;
   const int b = (int)(unit / upt);
   const long long in_seq = unit % upt;
+  ptx::pdl_wait();
   const span::Seq sq = span::seq_of(p.s, b);
   if (sq.tiles == 0) return;
   // where the unit's tiles lie in the list of all tiles
-  long long total = 0, before = 0;
-  for (int b0 = 0; b0 < p.s.B; b0 += 32) {
-    long long n = 0;
-    if (b0 + lane < p.s.B) n = span::seq_of(p.s, b0 + lane).tiles * upt;
-    long long nb = b0 + lane < b ? n : 0;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      n += __shfl_xor_sync(0xffffffffu, n, o);
-      nb += __shfl_xor_sync(0xffffffffu, nb, o);
-    }
-    total += n;
-    before += nb;
-  }
+  long long total, before;
+  span::count_tiles(p.s, lane, b, false, &total, &before);
   const long long per = max(1LL, (total + grid_tc - 1) / grid_tc);
   const long long u0 = before + in_seq * sq.tiles, u1 = u0 + sq.tiles;
   const long long c0 = u0 / per, c1 = (u1 - 1) / per;
@@ -706,9 +694,8 @@ cudaError_t launch_span_tc(const hata_dims_t& d, const span::Params& s, const Pa
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long units = (long long)d.batch * d.n_kv_heads * p.s.row_tiles;
   if (units > 0x7fffffffLL) return cudaErrorNotSupported;
-  span_merge_kernel<<<dim3((unsigned)units, kHeadDim / 4 / kMergeCols, p.pair ? 2 : 1), kTcTile * kMergeCols, 0, st>>>(
-      p, sms, rows);
-  return cudaGetLastError();
+  return launch_early(span_merge_kernel, dim3((unsigned)units, kHeadDim / 4 / kMergeCols, p.pair ? 2 : 1),
+                      kTcTile * kMergeCols, st, p, sms, rows);
 }
 
 cudaError_t launch_window_prefill(const hata_dims_t& d, const void* q, const void* K, const void* V,

@@ -58,7 +58,7 @@ def window_case(H, dtype, B, Hq, Hkv, max_seq, bs, window, sink, lens, seed=0):
     lens_d = torch.tensor(lens, dtype=torch.int32, device="cuda")
     out = torch.full((B, Hq, D), 9.0, device="cuda", dtype=dtype)
     ws = c.workspace()
-    for _ in range(2):  # the second call finds the counters that the first one left
+    for _ in range(2):  # the second call finds what the first one left in the workspace
         if bs:
             K, V = c.pools()
             H.hata_window_decode_paged(c.d, q, K, V, c.bt, bs, lens_d, window, sink, 0.0, out, ws)
@@ -71,7 +71,6 @@ def window_case(H, dtype, B, Hq, Hkv, max_seq, bs, window, sink, lens, seed=0):
                 rows = slice(g * G, (g + 1) * G)
                 want, absv, qk = attend(q[b, rows], c.K[b, g], c.V[b, g], sees[b][None].expand(G, max_seq))
                 close(out[b, rows], want, absv, qk, min(L, window + sink), dtype)
-    assert not bool(ws[256:].view(torch.int32)[: B * Hkv].any())
 
 
 DTYPES = [torch.float32, torch.bfloat16]
