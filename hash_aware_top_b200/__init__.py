@@ -221,8 +221,14 @@ def _check(status: int, where: str):
         raise HataError(status, where)
 
 
+# The current stream's handle without a Stream object around it, which costs 3 us to make (60 ns this way).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
@@ -493,62 +499,75 @@ def hata_decode_step_paged(dims: Dims, q, K_pool, V_pool, W_q, W_k, codes_pool, 
 # --- serving operators beside the decode step -----------------------------------------------------------
 
 
-def _dptr(t, name, shape, dtype, optional=False):
-    """Device address of a contiguous tensor of this shape and type on the current device (None if optional)."""
+def _device() -> int:
+    """The current device; where there is none, a number that no tensor has."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
+
+
+def _dptr(t, name, shape, dtype, dev, optional=False):
+    """Address of a contiguous tensor of this shape and type on the current device `dev` (None if optional)."""
+    if t is None and optional:
+        return None
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        return t.data_ptr()
     if t is None:
-        if optional:
-            return None
         raise ValueError(f"{name} is required")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device (got {t.device})")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _ws(ws):
+def _ws(ws, dev):
     """Address and size of a uint8 workspace on the current device."""
-    return _dptr(ws, "workspace", ws.shape if isinstance(ws, torch.Tensor) else None, torch.uint8), ws.numel()
+    n = ws.numel() if isinstance(ws, torch.Tensor) else 0
+    return _dptr(ws, "workspace", (n,), torch.uint8, dev), n
 
 
-def _token_rows(t, name, d: Dims, heads: int, n_tok: int):
+def _token_rows(t, name, d: Dims, heads: int, n_tok: int, dev):
     """Address and token stride of [B][n_tok][heads][d], heads contiguous, tokens at any one stride (a part of a
     projection's output, for instance)."""
-    shape = (d.batch, n_tok, heads, d.head_dim)
+    B, D = d.batch, d.head_dim
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device (got {t.device})")
     if t.dtype is not d.torch_dtype:
         raise TypeError(f"{name} must be {d.torch_dtype} (got {t.dtype})")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape} (got {tuple(t.shape)})")
+    if t.shape != (B, n_tok, heads, D):
+        raise ValueError(f"{name} must have shape {(B, n_tok, heads, D)} (got {tuple(t.shape)})")
     sb, st, sh, se = t.stride()
-    stride = st if n_tok > 1 else sb if d.batch > 1 else heads * d.head_dim
-    if (se != 1 or (heads > 1 and sh != d.head_dim) or (n_tok > 1 and d.batch > 1 and sb != n_tok * st)):
-        raise ValueError(f"{name} must hold each token's heads side by side and its tokens at one stride (strides {t.stride()})")
-    return t.data_ptr(), stride
+    if se != 1 or (heads > 1 and sh != D) or (n_tok > 1 and B > 1 and sb != n_tok * st):
+        raise ValueError(f"{name} must hold each token's heads side by side and its tokens at one stride "
+                         f"(strides {t.stride()})")
+    return t.data_ptr(), st if n_tok > 1 else sb if B > 1 else heads * D
 
 
-def _cache_args(d: Dims, K, V, block_table=None, block_size=None):
-    """Addresses of a cache, and of its table where it is paged."""
-    if block_table is None:
-        shape = (d.batch, d.n_kv_heads, d.max_seq, d.head_dim)
-        return (_dptr(K, "K", shape, d.torch_dtype), _dptr(V, "V", shape, d.torch_dtype))
+def _cache_args(d: Dims, dev, K, V):
+    """Addresses of a contiguous cache."""
+    shape, t = (d.batch, d.n_kv_heads, d.max_seq, d.head_dim), d.torch_dtype
+    return _dptr(K, "K", shape, t, dev), _dptr(V, "V", shape, t, dev)
+
+
+def _pool_args(d: Dims, dev, K_pool, V_pool, block_table, block_size):
+    """Addresses of paged pools and of their table."""
     bs = int(block_size)
-    if not isinstance(K, torch.Tensor) or K.dim() != 4:
+    if not isinstance(K_pool, torch.Tensor) or K_pool.dim() != 4:
         raise ValueError("K_pool must be a tensor [n_blocks][Hkv][block_size][d]")
-    n_blocks = K.shape[0]
+    n_blocks, t = K_pool.shape[0], d.torch_dtype
     pool = (n_blocks, d.n_kv_heads, bs, d.head_dim)
-    table = (d.batch, -(-d.max_seq // bs) if bs > 0 else 0)
-    return (_dptr(K, "K_pool", pool, d.torch_dtype), _dptr(V, "V_pool", pool, d.torch_dtype),
-            _dptr(block_table, "block_table", table, torch.int32), bs, n_blocks)
+    return (_dptr(K_pool, "K_pool", pool, t, dev), _dptr(V_pool, "V_pool", pool, t, dev),
+            _dptr(block_table, "block_table", (d.batch, -(-d.max_seq // bs) if bs > 0 else 0), torch.int32, dev), bs,
+            n_blocks)
 
 
 def hata_rope_table(n_pos, rot_dim, theta, stream=None) -> torch.Tensor:
@@ -559,7 +578,7 @@ def hata_rope_table(n_pos, rot_dim, theta, stream=None) -> torch.Tensor:
     return table
 
 
-def _norm_rope_args(d, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions, seq_lens, q_out):
+def _norm_rope_args(d, dev, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions, seq_lens, q_out):
     if not isinstance(q_in, torch.Tensor) or q_in.dim() != 4:
         raise ValueError("q_in must be a tensor [B][n_tok][Hq][d]")
     T, w = q_in.shape[1], (d.head_dim,)
@@ -568,34 +587,36 @@ def _norm_rope_args(d, q_in, k_in, v_in, q_weight, k_weight, eps, table, interle
         if not isinstance(table, torch.Tensor) or table.dim() != 3:
             raise ValueError("table must be a tensor [n_pos][2][rot_dim / 2]")
         n_pos, rot = table.shape[0], 2 * table.shape[2]
-        table = _dptr(table, "table", (n_pos, 2, rot // 2), torch.float32)
-    return (ctypes.byref(d), T, *_token_rows(q_in, "q_in", d, d.n_q_heads, T), *_token_rows(k_in, "k_in", d, d.n_kv_heads, T),
-            *_token_rows(v_in, "v_in", d, d.n_kv_heads, T), _dptr(q_weight, "q_weight", w, torch.float32, True),
-            _dptr(k_weight, "k_weight", w, torch.float32, True), float(eps), table, n_pos, rot, int(bool(interleaved)),
-            _dptr(n_new, "n_new", (d.batch,), torch.int32, True),
-            _dptr(positions, "positions", (d.batch, T), torch.int32, True),
-            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32),
-            _dptr(q_out, "q_out", (d.batch, d.n_q_heads, T, d.head_dim), d.torch_dtype))
+        table = _dptr(table, "table", (n_pos, 2, rot // 2), torch.float32, dev)
+    return (ctypes.byref(d), T, *_token_rows(q_in, "q_in", d, d.n_q_heads, T, dev), *_token_rows(k_in, "k_in", d, d.n_kv_heads, T, dev),
+            *_token_rows(v_in, "v_in", d, d.n_kv_heads, T, dev), _dptr(q_weight, "q_weight", w, torch.float32, dev, True),
+            _dptr(k_weight, "k_weight", w, torch.float32, dev, True), float(eps), table, n_pos, rot, int(bool(interleaved)),
+            _dptr(n_new, "n_new", (d.batch,), torch.int32, dev, True),
+            _dptr(positions, "positions", (d.batch, T), torch.int32, dev, True),
+            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32, dev),
+            _dptr(q_out, "q_out", (d.batch, d.n_q_heads, T, d.head_dim), d.torch_dtype, dev))
 
 
 def hata_norm_rope(dims: Dims, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions,
                    seq_lens, q_out, K, V, ws, stream=None):
     """Norm and rotate the heads of q_in and k_in ([B][n_tok][heads][d], any token stride), writing q_out
     ([B][Hq][n_tok][d]) and the K and V cache rows of the new tokens, the last of seq_lens[b]."""
+    dev = _device()
     _check(
         lib.hata_norm_rope(
-            *_norm_rope_args(dims, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions,
-                             seq_lens, q_out), *_cache_args(dims, K, V), *_ws(ws), _stream(stream)),
+            *_norm_rope_args(dims, dev, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions,
+                             seq_lens, q_out), *_cache_args(dims, dev, K, V), *_ws(ws, dev), _stream(stream)),
         "hata_norm_rope")
 
 
 def hata_norm_rope_paged(dims: Dims, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions,
                          seq_lens, q_out, K_pool, V_pool, block_table, block_size, ws, stream=None):
     """hata_norm_rope into paged pools ([n_blocks][Hkv][block_size][d])."""
+    dev = _device()
     _check(
         lib.hata_norm_rope_paged(
-            *_norm_rope_args(dims, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions,
-                             seq_lens, q_out), *_cache_args(dims, K_pool, V_pool, block_table, block_size), *_ws(ws),
+            *_norm_rope_args(dims, dev, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions,
+                             seq_lens, q_out), *_pool_args(dims, dev, K_pool, V_pool, block_table, block_size), *_ws(ws, dev),
             _stream(stream)),
         "hata_norm_rope_paged")
 
@@ -610,12 +631,13 @@ def hata_span_workspace_size(dims: Dims, n_tok: int = 1) -> int:
 def hata_window_decode(dims: Dims, q, K, V, seq_lens, window, n_sink, scale, out, ws, stream=None):
     """Decode attention over the last `window` slots and the first `n_sink` of each sequence."""
     d = dims
+    dev = _device()
     row = (d.batch, d.n_q_heads, d.head_dim)
     _check(
         lib.hata_window_decode(
-            ctypes.byref(d), _dptr(q, "q", row, d.torch_dtype), *_cache_args(d, K, V),
-            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32), int(window), int(n_sink), float(scale),
-            _dptr(out, "out", row, d.torch_dtype), *_ws(ws), _stream(stream)),
+            ctypes.byref(d), _dptr(q, "q", row, d.torch_dtype, dev), *_cache_args(d, dev, K, V),
+            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32, dev), int(window), int(n_sink), float(scale),
+            _dptr(out, "out", row, d.torch_dtype, dev), *_ws(ws, dev), _stream(stream)),
         "hata_window_decode")
 
 
@@ -623,12 +645,13 @@ def hata_window_decode_paged(dims: Dims, q, K_pool, V_pool, block_table, block_s
                              out, ws, stream=None):
     """hata_window_decode over paged pools."""
     d = dims
+    dev = _device()
     row = (d.batch, d.n_q_heads, d.head_dim)
     _check(
         lib.hata_window_decode_paged(
-            ctypes.byref(d), _dptr(q, "q", row, d.torch_dtype), *_cache_args(d, K_pool, V_pool, block_table, block_size),
-            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32), int(window), int(n_sink), float(scale),
-            _dptr(out, "out", row, d.torch_dtype), *_ws(ws), _stream(stream)),
+            ctypes.byref(d), _dptr(q, "q", row, d.torch_dtype, dev), *_pool_args(d, dev, K_pool, V_pool, block_table, block_size),
+            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32, dev), int(window), int(n_sink), float(scale),
+            _dptr(out, "out", row, d.torch_dtype, dev), *_ws(ws, dev), _stream(stream)),
         "hata_window_decode_paged")
 
 
@@ -636,32 +659,34 @@ def hata_window_prefill(dims: Dims, q, K, V, seq_lens, window, n_sink, scale, ou
     """Causal prefill attention (q/out [B][Hq][max_seq][d], K/V [B][Hkv][max_seq][d], bf16) over the last `window`
     positions and the first `n_sink`."""
     d = dims
+    dev = _device()
     rows = (d.batch, d.n_q_heads, d.max_seq, d.head_dim)
     _check(
         lib.hata_window_prefill(
-            ctypes.byref(d), _dptr(q, "q", rows, d.torch_dtype), *_cache_args(d, K, V),
-            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32), int(window), int(n_sink), float(scale),
-            _dptr(out, "out", rows, d.torch_dtype), *_ws(ws), _stream(stream)),
+            ctypes.byref(d), _dptr(q, "q", rows, d.torch_dtype, dev), *_cache_args(d, dev, K, V),
+            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32, dev), int(window), int(n_sink), float(scale),
+            _dptr(out, "out", rows, d.torch_dtype, dev), *_ws(ws, dev), _stream(stream)),
         "hata_window_prefill")
 
 
-def _tree_args(d, q, seq_lens, n_new, mask, out):
+def _tree_args(d, dev, q, seq_lens, n_new, mask, out):
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a tensor [B][Hq][n_tok][d]")
     T = q.shape[2]
     rows = (d.batch, d.n_q_heads, T, d.head_dim)
     word = mask.dtype if isinstance(mask, torch.Tensor) and mask.dtype == torch.uint32 else torch.int32
-    return (T, _dptr(q, "q", rows, d.torch_dtype),
-            (_dptr(seq_lens, "seq_lens", (d.batch,), torch.int32), _dptr(n_new, "n_new", (d.batch,), torch.int32, True),
-             _dptr(mask, "mask", (d.batch, T, -(-T // 32)), word, True)), _dptr(out, "out", rows, d.torch_dtype))
+    return (T, _dptr(q, "q", rows, d.torch_dtype, dev),
+            (_dptr(seq_lens, "seq_lens", (d.batch,), torch.int32, dev), _dptr(n_new, "n_new", (d.batch,), torch.int32, dev, True),
+             _dptr(mask, "mask", (d.batch, T, -(-T // 32)), word, dev, True)), _dptr(out, "out", rows, d.torch_dtype, dev))
 
 
 def hata_tree_attention(dims: Dims, q, K, V, seq_lens, n_new, mask, scale, out, ws, stream=None):
     """Attention of the drafted tokens q ([B][Hq][n_tok][d]) over a cache that holds them: mask [B][n_tok][words]
     (int32 or uint32 bits: which drafted tokens each one sees), or None for a chain."""
-    T, pq, seqs, po = _tree_args(dims, q, seq_lens, n_new, mask, out)
+    dev = _device()
+    T, pq, seqs, po = _tree_args(dims, dev, q, seq_lens, n_new, mask, out)
     _check(
-        lib.hata_tree_attention(ctypes.byref(dims), T, pq, *_cache_args(dims, K, V), *seqs, float(scale), po, *_ws(ws),
+        lib.hata_tree_attention(ctypes.byref(dims), T, pq, *_cache_args(dims, dev, K, V), *seqs, float(scale), po, *_ws(ws, dev),
                                 _stream(stream)),
         "hata_tree_attention")
 
@@ -669,11 +694,12 @@ def hata_tree_attention(dims: Dims, q, K, V, seq_lens, n_new, mask, scale, out, 
 def hata_tree_attention_paged(dims: Dims, q, K_pool, V_pool, block_table, block_size, seq_lens, n_new, mask, scale,
                               out, ws, stream=None):
     """hata_tree_attention over paged pools."""
-    T, pq, seqs, po = _tree_args(dims, q, seq_lens, n_new, mask, out)
+    dev = _device()
+    T, pq, seqs, po = _tree_args(dims, dev, q, seq_lens, n_new, mask, out)
     _check(
         lib.hata_tree_attention_paged(ctypes.byref(dims), T, pq,
-                                      *_cache_args(dims, K_pool, V_pool, block_table, block_size), *seqs, float(scale),
-                                      po, *_ws(ws), _stream(stream)),
+                                      *_pool_args(dims, dev, K_pool, V_pool, block_table, block_size), *seqs, float(scale),
+                                      po, *_ws(ws, dev), _stream(stream)),
         "hata_tree_attention_paged")
 
 
@@ -683,59 +709,62 @@ def hata_pages_workspace_size(dims: Dims) -> int:
     return n.value
 
 
-def _table_args(d, block_table, block_size):
+def _table_args(d, dev, block_table, block_size):
     bs = int(block_size)
-    return _dptr(block_table, "block_table", (d.batch, -(-d.max_seq // bs) if bs > 0 else 0), torch.int32), bs
+    return _dptr(block_table, "block_table", (d.batch, -(-d.max_seq // bs) if bs > 0 else 0), torch.int32, dev), bs
 
 
 def hata_pages_fork(dims: Dims, parent, block_table, block_size, seq_lens, ref_count, ws, stream=None):
     """Row b of the table takes the pages and the length of row parent[b] (< 0 or b: unchanged); pages are shared."""
     d = dims
-    table, bs = _table_args(d, block_table, block_size)
+    dev = _device()
+    table, bs = _table_args(d, dev, block_table, block_size)
     n_blocks = ref_count.numel() if isinstance(ref_count, torch.Tensor) else 0
     _check(
         lib.hata_pages_fork(
-            ctypes.byref(d), _dptr(parent, "parent", (d.batch,), torch.int32), table, bs, n_blocks,
-            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32),
-            _dptr(ref_count, "ref_count", (n_blocks,), torch.int32), *_ws(ws), _stream(stream)),
+            ctypes.byref(d), _dptr(parent, "parent", (d.batch,), torch.int32, dev), table, bs, n_blocks,
+            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32, dev),
+            _dptr(ref_count, "ref_count", (n_blocks,), torch.int32, dev), *_ws(ws, dev), _stream(stream)),
         "hata_pages_fork")
 
 
-def _codes_args(codes, d, lead):
-    return _dptr(codes, "codes", d.code_shape(*lead), _codes_dtype(codes, d), True)
+def _codes_args(codes, d, dev, lead):
+    return _dptr(codes, "codes", d.code_shape(*lead), _codes_dtype(codes, d), dev, True)
 
 
 def hata_pages_resize(dims: Dims, new_lens, K_pool, V_pool, codes_pool, block_table, block_size, seq_lens, ref_count,
                       ws, stream=None):
     """Every sequence to new_lens[b]: pages freed, a shared partial last page copied before it grows, pages added."""
     d = dims
-    pk, pv, table, bs, n_blocks = _cache_args(d, K_pool, V_pool, block_table, block_size)
+    dev = _device()
+    pk, pv, table, bs, n_blocks = _pool_args(d, dev, K_pool, V_pool, block_table, block_size)
     _check(
         lib.hata_pages_resize(
-            ctypes.byref(d), _dptr(new_lens, "new_lens", (d.batch,), torch.int32), pk, pv,
-            _codes_args(codes_pool, d, (n_blocks, d.n_kv_heads, bs)), table, bs, n_blocks,
-            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32),
-            _dptr(ref_count, "ref_count", (n_blocks,), torch.int32), *_ws(ws), _stream(stream)),
+            ctypes.byref(d), _dptr(new_lens, "new_lens", (d.batch,), torch.int32, dev), pk, pv,
+            _codes_args(codes_pool, d, dev, (n_blocks, d.n_kv_heads, bs)), table, bs, n_blocks,
+            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32, dev),
+            _dptr(ref_count, "ref_count", (n_blocks,), torch.int32, dev), *_ws(ws, dev), _stream(stream)),
         "hata_pages_resize")
 
 
-def _keep_args(d, keep, n_keep, n_new, seq_lens):
+def _keep_args(d, dev, keep, n_keep, n_new, seq_lens):
     if not isinstance(keep, torch.Tensor) or keep.dim() != 2:
         raise ValueError("keep must be a tensor [B][n_tok]")
     T, b = keep.shape[1], (d.batch,)
-    return (T, _dptr(keep, "keep", (d.batch, T), torch.int32), _dptr(n_keep, "n_keep", b, torch.int32),
-            _dptr(n_new, "n_new", b, torch.int32, True), _dptr(seq_lens, "seq_lens", b, torch.int32))
+    return (T, _dptr(keep, "keep", (d.batch, T), torch.int32, dev), _dptr(n_keep, "n_keep", b, torch.int32, dev),
+            _dptr(n_new, "n_new", b, torch.int32, dev, True), _dptr(seq_lens, "seq_lens", b, torch.int32, dev))
 
 
 def hata_compact_kv(dims: Dims, keep, n_keep, n_new, seq_lens, K, V, codes, new_lens, ws, stream=None):
     """Of the newest n_new[b] tokens keep rows keep[b][:n_keep[b]] (ascending), moved to the front of them in K, V and
     codes (or None); new_lens[b] (or None) receives the length that is left."""
     d = dims
+    dev = _device()
     _check(
         lib.hata_compact_kv(
-            ctypes.byref(d), *_keep_args(d, keep, n_keep, n_new, seq_lens), *_cache_args(d, K, V),
-            _codes_args(codes, d, (d.batch, d.n_kv_heads, d.max_seq)),
-            _dptr(new_lens, "new_lens", (d.batch,), torch.int32, True), *_ws(ws), _stream(stream)),
+            ctypes.byref(d), *_keep_args(d, dev, keep, n_keep, n_new, seq_lens), *_cache_args(d, dev, K, V),
+            _codes_args(codes, d, dev, (d.batch, d.n_kv_heads, d.max_seq)),
+            _dptr(new_lens, "new_lens", (d.batch,), torch.int32, dev, True), *_ws(ws, dev), _stream(stream)),
         "hata_compact_kv")
 
 
@@ -743,12 +772,13 @@ def hata_compact_kv_paged(dims: Dims, keep, n_keep, n_new, seq_lens, K_pool, V_p
                           block_size, new_lens, ws, stream=None):
     """hata_compact_kv over paged pools."""
     d = dims
-    pk, pv, table, bs, n_blocks = _cache_args(d, K_pool, V_pool, block_table, block_size)
+    dev = _device()
+    pk, pv, table, bs, n_blocks = _pool_args(d, dev, K_pool, V_pool, block_table, block_size)
     _check(
         lib.hata_compact_kv_paged(
-            ctypes.byref(d), *_keep_args(d, keep, n_keep, n_new, seq_lens), pk, pv,
-            _codes_args(codes_pool, d, (n_blocks, d.n_kv_heads, bs)), table, bs, n_blocks,
-            _dptr(new_lens, "new_lens", (d.batch,), torch.int32, True), *_ws(ws), _stream(stream)),
+            ctypes.byref(d), *_keep_args(d, dev, keep, n_keep, n_new, seq_lens), pk, pv,
+            _codes_args(codes_pool, d, dev, (n_blocks, d.n_kv_heads, bs)), table, bs, n_blocks,
+            _dptr(new_lens, "new_lens", (d.batch,), torch.int32, dev, True), *_ws(ws, dev), _stream(stream)),
         "hata_compact_kv_paged")
 
 

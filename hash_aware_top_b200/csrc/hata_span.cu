@@ -29,6 +29,9 @@ using namespace span;
 constexpr int kSpThreads = 256;
 constexpr int kSpWarps = kSpThreads / 32;
 constexpr int kSpKeys = 16;  // slots of a warp in a tile
+// Registers of a thread: 256 x 224 of the SM's 65536 leave room for a CTA of the joining kernel (128 x 48), which is
+// then there, its prologue done, when the main kernel ends.
+constexpr int kSpRegs = 224;
 constexpr float kSpSlack = 8.f;  // log2 units
 static_assert(kSpWarps * kSpKeys == kSpanTile, "the warps share a tile");
 
@@ -102,22 +105,21 @@ __device__ __forceinline__ void join_weights(float* sm_m, const float* sm_l, int
 
 constexpr int kOutRow = kHeadDim + 8;  // floats of a row of a warp's output in shared memory: rows on distinct banks
 
-// A partial: m [ROWS], l [ROWS], O [ROWS][128].  A CTA continues one unit at most (slot 0) and leaves one at most (1).
+// A partial: m [ROWS], l [ROWS], O [ROWS][128].
 template <int ROWS>
-__device__ __forceinline__ float* part_of(const Params& p, long long cta, long long per, long long u0) {
-  return p.part + ((size_t)cta * 2 + (cta * per > u0 ? 0 : 1)) * ROWS * (kHeadDim + 2);
+__device__ __forceinline__ float* part_of(const Params& p, int slot) {
+  return p.part + (size_t)slot * ROWS * (kHeadDim + 2);
 }
 
 // The end of a unit's run in this CTA.  In shared memory: m, l [kSpWarps][ROWS] and o [kSpWarps][ROWS][kOutRow]
 // of the warps.  Joins them, then writes the rows of a unit that is all this CTA's, or leaves a partial.
 template <typename T, int ROWS>
-__device__ __forceinline__ void finish_unit(const Params& p, float* sm_m, float* sm_l, const float* sm_o, int b, int n_b,
-                                            int g, int rt, long long u0, long long u1, long long per) {
+__device__ __forceinline__ void finish_unit(const Params& p, float* sm_m, float* sm_l, const float* sm_o,
+                                            const Piece& pc, int g, int rt) {
   __shared__ float row_m[ROWS], row_l[ROWS];
   const int tid = threadIdx.x, r0 = rt * ROWS;
-  const bool whole = u0 / per == (u1 - 1) / per;
-  T* out = static_cast<T*>(p.out) + (((size_t)b * p.Hq + (size_t)g * p.G) * p.T + r0) * kHeadDim;
-  float* part = part_of<ROWS>(p, blockIdx.x, per, u0);
+  T* out = static_cast<T*>(p.out) + (((size_t)pc.b * p.Hq + (size_t)g * p.G) * p.T + r0) * kHeadDim;
+  float* part = part_of<ROWS>(p, pc.slot);
   join_weights<ROWS>(sm_m, sm_l, kSpWarps, row_m, row_l);
   for (int e = tid; e < ROWS * kHeadDim / 4; e += kSpThreads) {
     const int r = e / (kHeadDim / 4), c = e % (kHeadDim / 4);
@@ -131,15 +133,15 @@ __device__ __forceinline__ void finish_unit(const Params& p, float* sm_m, float*
       o.z = fmaf(v.z, f, o.z);
       o.w = fmaf(v.w, f, o.w);
     }
-    if (whole) {
+    if (pc.whole) {
       const float l = row_l[r], inv = l == 0.f ? 0.f : 1.f / l;
-      if (r0 + r < p.R && (r0 + r) % p.T < n_b)
+      if (r0 + r < p.R && (r0 + r) % p.T < pc.seq.n_b)
         store4<T>(out + 4 * e, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     } else {
       reinterpret_cast<float4*>(part + 2 * ROWS)[e] = o;
     }
   }
-  if (!whole && tid < ROWS) {
+  if (!pc.whole && tid < ROWS) {
     part[tid] = row_m[tid];
     part[ROWS + tid] = row_l[tid];
   }
@@ -151,23 +153,21 @@ constexpr int kJoinWarps = 4;
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(kJoinWarps * 32) span_join_kernel(const Params p, int grid_main) {
   const int lane = threadIdx.x & 31, r = (int)blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-  const long long upt = (long long)p.Hkv * p.row_tiles, unit = blockIdx.x, in_seq = unit % upt;
-  const int b = (int)(unit / upt), g = (int)(in_seq % p.Hkv), row = (int)(in_seq / p.Hkv) * ROWS + r;
-  ptx::pdl_wait();
+  const int upt = p.Hkv * p.row_tiles, b = (int)blockIdx.x / upt, in_seq = (int)blockIdx.x % upt;
+  const int g = in_seq % p.Hkv, row = in_seq / p.Hkv * ROWS + r;
+  // the lengths are the call's inputs: where the partials lie is found while the main kernel still runs
   const Seq sq = seq_of(p, b);
   if (sq.tiles == 0 || row >= p.R || row % p.T >= sq.n_b) return;
-  long long total, before;
-  count_tiles(p, lane, b, false, &total, &before);
-  const long long per = max(1LL, (total + grid_main - 1) / grid_main);
-  const long long u0 = before + in_seq * sq.tiles, c0 = u0 / per, c1 = (u0 + sq.tiles - 1) / per;
-  if (c0 == c1) return;  // written by the one CTA that had it
-  const int n = (int)(c1 - c0) + 1;
+  const Runs runs = runs_of(p, lane, grid_main, b, in_seq, sq);
+  const int n = runs.n;
+  if (n == 1) return;  // written by the one CTA that had it
+  ptx::pdl_wait();
   float M = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = 0; i0 < n; i0 += 32) {  // 32 runs: a lane per run for the weights, then a lane per column for O
     float m = -INFINITY, li = 0.f;
     if (i0 + lane < n) {
-      const float* pp = part_of<ROWS>(p, c0 + i0 + lane, per, u0);
+      const float* pp = part_of<ROWS>(p, runs.slot(i0 + lane));
       m = __ldcg(pp + r);
       li = __ldcg(pp + ROWS + r);
     }
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) span_join_kernel(const Params
 #pragma unroll 8
     for (int k = 0; k < k1; ++k) {
       const float fk = __shfl_sync(0xffffffffu, f, k);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of<ROWS>(p, c0 + i0 + k, per, u0) + 2 * ROWS) +
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of<ROWS>(p, runs.slot(i0 + k)) + 2 * ROWS) +
                               r * (kHeadDim / 4) + lane);
       o.x = fmaf(v.x, fk, o.x);
       o.y = fmaf(v.y, fk, o.y);
@@ -220,7 +220,7 @@ struct SimtSmem {
 };
 
 template <int ROWS, bool PAGED>
-__global__ void __launch_bounds__(kSpThreads, 1) span_simt_kernel(const Params p) {
+__global__ void __maxnreg__(kSpRegs) span_simt_kernel(const Params p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   using S = SimtSmem<ROWS>;
   using T = float;
@@ -234,21 +234,13 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_simt_kernel(const Params p
   float* sm_p = reinterpret_cast<float*>(smem + S::kP) + warp * ROWS * kSpKeys;
 
   ptx::pdl_launch_dependents();  // the joining kernel may be set up; it waits for this one to end
-  long long at, end, per;
-  Cursor cur;
-  if (!my_run(p, lane, blockIdx.x == 0 && warp == 0, &at, &end, &per, &cur)) return;
+  Walker walk;
+  walk.begin(p, lane, blockIdx.x == 0 && warp == 0);
   const int key = lane & 15, half = lane >> 4;
-  while (at < end) {
-    while (at >= cur.seq_start + (long long)cur.seq.tiles * p.Hkv * p.row_tiles) {
-      cur.seq_start += (long long)cur.seq.tiles * p.Hkv * p.row_tiles;
-      cur.seq = seq_of(p, ++cur.b);
-    }
-    const int b = cur.b;
-    const Seq& sq = cur.seq;
-    const long long in_seq = (at - cur.seq_start) / sq.tiles;  // unit within the sequence
-    const int g = (int)(in_seq % p.Hkv), rt = (int)(in_seq / p.Hkv);
-    const long long u0 = cur.seq_start + in_seq * sq.tiles, u1 = u0 + sq.tiles;
-    const int j0 = (int)(at - u0), j1 = (int)(min(end, u1) - u0);
+  Piece pc;
+  while (walk.next(p, pc)) {
+    const int b = pc.b, g = pc.in_seq % p.Hkv, rt = pc.in_seq / p.Hkv, j0 = pc.j0, j1 = pc.j1;
+    const Seq& sq = pc.seq;
     const int r0 = rt * ROWS;
     // queries of this unit's rows (zeros past the last)
     const T* q = static_cast<const T*>(p.q) + (((size_t)b * p.Hq + (size_t)g * p.G) * p.T + r0) * kHeadDim;
@@ -346,9 +338,8 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_simt_kernel(const Params p
           make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
     }
     __syncthreads();
-    finish_unit<T, ROWS>(p, sm_m, sm_l, sm_o, b, sq.n_b, g, rt, u0, u1, per);
+    finish_unit<T, ROWS>(p, sm_m, sm_l, sm_o, pc, g, rt);
     __syncthreads();
-    at = u0 + j1;
   }
 }
 
@@ -393,7 +384,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 }
 
 template <int MT, bool PAGED>
-__global__ void __launch_bounds__(kSpThreads, 1) span_mma_kernel(const Params p) {
+__global__ void __maxnreg__(kSpRegs) span_mma_kernel(const Params p) {
   extern __shared__ __align__(1024) unsigned char smem[];
   using S = MmaSmem<MT>;
   constexpr int ROWS = S::kRows;
@@ -413,20 +404,12 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_mma_kernel(const Params p)
   const uint32_t vfrag = (uint32_t)(vkey * kMmRowB + (((lane >> 4) ^ (vkey & 7)) << 4)) + kSpKeys * kMmRowB;
 
   ptx::pdl_launch_dependents();  // the joining kernel may be set up; it waits for this one to end
-  long long at, end, per;
-  Cursor cur;
-  if (!my_run(p, lane, blockIdx.x == 0 && warp == 0, &at, &end, &per, &cur)) return;
-  while (at < end) {
-    while (at >= cur.seq_start + (long long)cur.seq.tiles * p.Hkv * p.row_tiles) {
-      cur.seq_start += (long long)cur.seq.tiles * p.Hkv * p.row_tiles;
-      cur.seq = seq_of(p, ++cur.b);
-    }
-    const int b = cur.b;
-    const Seq& sq = cur.seq;
-    const long long in_seq = (at - cur.seq_start) / sq.tiles;  // unit within the sequence
-    const int g = (int)(in_seq % p.Hkv), rt = (int)(in_seq / p.Hkv);
-    const long long u0 = cur.seq_start + in_seq * sq.tiles, u1 = u0 + sq.tiles;
-    const int j0 = (int)(at - u0), j1 = (int)(min(end, u1) - u0);
+  Walker walk;
+  walk.begin(p, lane, blockIdx.x == 0 && warp == 0);
+  Piece pc;
+  while (walk.next(p, pc)) {
+    const int b = pc.b, g = pc.in_seq % p.Hkv, rt = pc.in_seq / p.Hkv, j0 = pc.j0, j1 = pc.j1;
+    const Seq& sq = pc.seq;
     const int r0 = rt * ROWS;
     auto first_slot = [&](int j) {
       return (j < sq.sink_tiles ? j : sq.win_tile + j - sq.sink_tiles) * kSpanTile + warp * kSpKeys;
@@ -612,9 +595,8 @@ __global__ void __launch_bounds__(kSpThreads, 1) span_mma_kernel(const Params p)
               make_float2(o[mt][n][2 * h], o[mt][n][2 * h + 1]);
       }
     __syncthreads();
-    finish_unit<__nv_bfloat16, ROWS>(p, sm_m, sm_l, sm_o, b, sq.n_b, g, rt, u0, u1, per);
+    finish_unit<__nv_bfloat16, ROWS>(p, sm_m, sm_l, sm_o, pc, g, rt);
     __syncthreads();
-    at = u0 + j1;
   }
 }
 
@@ -643,7 +625,7 @@ cudaError_t launch_rows(Kernel k, int smem, Params p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   p.row_tiles = (p.R + ROWS - 1) / ROWS;
   const long long units = (long long)p.B * p.Hkv * p.row_tiles;
-  if (units > 0x7fffffffLL) return cudaErrorNotSupported;
+  if (!span_fits(p, units)) return cudaErrorNotSupported;
   const int grid = span_sms();
   k<<<grid, kSpThreads, smem, st>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -5,8 +5,8 @@
 // head of the group, new token) pairs, which lie next to each other in q and out.  Its keys are a
 // list of tiles of kSpanTile cache slots: all of [0, L) for a tree; the tiles that hold sinks, then
 // those that hold the window, for a window.  The tiles of all units, in the order (b, row tile, g, tile), are
-// cut into equal runs, one per CTA, so ragged lengths keep every SM busy to the end; a CTA's run may
-// end one unit and begin the next.  A unit that one CTA covers is written at once.  Otherwise each of
+// shared out over the CTAs (Split below), so ragged lengths keep every SM busy to the end.  A unit that one CTA
+// covers is written at once.  Otherwise each of
 // its CTAs leaves a partial (row maximum, row sum, weighted values; fp32) in the workspace, and a second kernel,
 // launched early (programmatic dependent launch), joins them in the order of the split.  Joining them in
 // the last CTA to arrive was slower: one SM then reads all partials of a unit (15 us for 32 rows and 19 runs).
@@ -74,70 +74,196 @@ __device__ __forceinline__ Seq seq_of(const Params& p, int b) {
   return s;
 }
 
-// Where a CTA stands in the list of tiles (the same in every thread of a warp).
-struct Cursor {
-  int b;                // sequence
-  Seq seq;
-  long long seq_start;  // first tile of the sequence in the list of all tiles
+// How the tiles are shared out.  Two ways, and every warp that needs to know works out the same one:
+//   flat     CTA c takes tiles c * per .. of the list of all tiles; a run may end one unit and begin another, which
+//            costs about kSwitchTiles tiles of time (the pipeline drains, rows are written, queries are loaded)
+//   aligned  each unit of sequence b gets k_b CTAs of its own, in proportion to its tiles (1 + its share of
+//            the CTAs that are more than units), so no run changes its unit, but some CTAs are idle
+// Aligned is taken when its longest run is no longer than a flat one and a change of unit: 8 units of 256 tiles
+// on 148 SMs take 14.2 tiles each, 8 x 18 runs of 14.2 against 148 runs of 13.8 tiles, most with a change.
+constexpr int kSwitchTiles = 3;
+
+struct Split {
+  int total;     // tiles of all units
+  int per;       // flat: tiles of a run
+  int units;     // of sequences with tiles
+  int my_tiles;  // with at most 32 sequences: of sequence `lane`
+  bool aligned;
 };
 
-__device__ __forceinline__ long long warp_sum(long long v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+__device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
+// aligned: CTAs of a unit.  32-bit: a unit has at most 2^24 tiles, a GPU at most 255 SMs (both checked on the host).
+__device__ __forceinline__ int ctas_of(const Split& sp, int tiles, int grid) {
+  return tiles == 0 ? 0 : min(tiles, 1 + (int)((unsigned)tiles * (unsigned)(grid - sp.units) / (unsigned)sp.total));
 }
 
-// Tiles of all units, and of the units of sequences before b.  All lanes of a warp; every warp that needs them
-// computes them, 32 sequences at a time, so no barrier is needed.
-__device__ __forceinline__ void count_tiles(const Params& p, int lane, int b, bool flag, long long* total,
-                                            long long* before) {
-  const long long per_tile = (long long)p.Hkv * p.row_tiles;
-  *total = *before = 0;
+// Tiles of each unit of sequence b0 + lane.
+__device__ __forceinline__ int tiles_at(const Params& p, const Split& sp, int b0, int lane) {
+  if (p.B <= 32) return sp.my_tiles;
+  return b0 + lane < p.B ? seq_of(p, b0 + lane).tiles : 0;
+}
+
+// All lanes of a warp.  The number of all tiles fits an int (checked on the host).
+__device__ __forceinline__ Split split_of(const Params& p, int lane, int grid, bool flag) {
+  Split sp;
+  sp.total = sp.units = sp.my_tiles = 0;
+  const int upt = p.Hkv * p.row_tiles;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    long long n = 0;
+    int n = 0;
     if (b0 + lane < p.B) {
       const Seq s = seq_of(p, b0 + lane);
-      n = s.tiles * per_tile;
+      n = s.tiles;
       if (s.bad && flag) set_status(p.status, HATA_ERR_INVALID_ARG);
     }
-    if (b0 < b) *before += warp_sum(b0 + lane < b ? n : 0);
-    *total += warp_sum(n);
+    sp.my_tiles = n;
+    sp.total += warp_sum(n) * upt;
+    sp.units += __popc(__ballot_sync(0xffffffffu, n > 0)) * upt;
   }
+  sp.per = max(1, (int)((unsigned)(sp.total + grid - 1) / (unsigned)grid));
+  sp.aligned = false;
+  if (sp.units > 0 && sp.units <= grid) {
+    int longest = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int tiles = tiles_at(p, sp, b0, lane), k = ctas_of(sp, tiles, grid);
+      longest = max(longest, __reduce_max_sync(0xffffffffu, k ? (int)((unsigned)(tiles + k - 1) / (unsigned)k) : 0));
+    }
+    sp.aligned = longest <= sp.per + kSwitchTiles;
+  }
+  return sp;
 }
 
-// This CTA's run [*at, *end) of the list of all tiles, each CTA's length *per, and the sequence it begins in.
-// False: the CTA has none.
-__device__ __forceinline__ bool my_run(const Params& p, int lane, bool flag, long long* at, long long* end,
-                                       long long* per, Cursor* c) {
-  long long total, before;
-  count_tiles(p, lane, 0, flag, &total, &before);
-  *per = max(1LL, (total + gridDim.x - 1) / gridDim.x);
-  *at = (long long)blockIdx.x * *per;
-  *end = min(total, *at + *per);
-  if (*at >= *end) return false;
-  c->b = 0;
-  c->seq_start = 0;
-  const long long per_tile = (long long)p.Hkv * p.row_tiles;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    long long n = 0;
-    if (b0 + lane < p.B) n = seq_of(p, b0 + lane).tiles * per_tile;
-    long long incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, c->seq_start + incl > *at);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      c->b = b0 + l;
-      c->seq_start += __shfl_sync(0xffffffffu, incl - n, l);
-      break;
-    }
-    c->seq_start += __shfl_sync(0xffffffffu, incl, 31);
+// Sum over the sequences before b of their tiles (flat) or CTAs (aligned).
+__device__ __forceinline__ int before(const Params& p, const Split& sp, int lane, int grid, int b) {
+  int sum = 0;
+  const int upt = p.Hkv * p.row_tiles;
+  for (int b0 = 0; b0 < b; b0 += 32) {
+    const int tiles = tiles_at(p, sp, b0, lane);
+    sum += warp_sum(b0 + lane < b ? (sp.aligned ? ctas_of(sp, tiles, grid) : tiles) * upt : 0);
   }
-  c->seq = seq_of(p, c->b);
-  return true;
+  return sum;
+}
+
+// A run of one unit's tiles.
+struct Piece {
+  int b, in_seq;  // sequence, unit within it
+  Seq seq;
+  int j0, j1;     // of the unit's list of tiles
+  int cta;        // this CTA
+  bool whole;     // all of the unit
+  int slot;       // of its partial: a CTA continues one unit at most (2 cta), and leaves one at most (2 cta + 1)
+};
+
+// The runs of this CTA, one after another.  All lanes of a warp.
+struct Walker {
+  Split sp;
+  int at, end;  // flat: of the list of all tiles
+  int b, base;  // sequence, and its first tile (flat)
+  Seq seq;
+  bool one;     // aligned: a run is left
+  Piece only;
+
+  __device__ __forceinline__ void begin(const Params& p, int lane, bool flag) {
+    const int grid = (int)gridDim.x, cta = (int)blockIdx.x, upt = p.Hkv * p.row_tiles;
+    sp = split_of(p, lane, grid, flag);
+    one = false;
+    at = sp.aligned ? cta : cta * sp.per;  // cta * per < total + per * grid
+    end = sp.aligned ? 0 : min(sp.total, at + sp.per);
+    if (!sp.aligned && at >= end) return;
+    // the sequence that holds tile (or CTA) `at`
+    b = base = 0;
+    bool found = false;
+    for (int b0 = 0; b0 < p.B && !found; b0 += 32) {
+      const int tiles = tiles_at(p, sp, b0, lane);
+      const int n = (sp.aligned ? ctas_of(sp, tiles, grid) : tiles) * upt;
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, base + incl > at);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        b = b0 + l;
+        base += __shfl_sync(0xffffffffu, incl - n, l);
+        found = true;
+      } else {
+        base += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    if (!found) {  // aligned: more CTAs than runs
+      end = at;
+      return;
+    }
+    seq = seq_of(p, b);
+    if (sp.aligned) {
+      const unsigned k = (unsigned)ctas_of(sp, seq.tiles, grid), part = (unsigned)(at - base) % k;
+      only.b = b;
+      only.in_seq = (int)((unsigned)(at - base) / k);
+      only.seq = seq;
+      only.j0 = (int)((unsigned)seq.tiles * part / k);
+      only.j1 = (int)((unsigned)seq.tiles * (part + 1) / k);
+      only.cta = cta;
+      only.whole = k == 1;
+      only.slot = 2 * cta;
+      one = true;
+      end = at;
+    }
+  }
+
+  __device__ __forceinline__ bool next(const Params& p, Piece& s) {
+    if (one) {
+      s = only;
+      one = false;
+      return true;
+    }
+    if (at >= end) return false;
+    const int upt = p.Hkv * p.row_tiles;
+    while (at >= base + seq.tiles * upt) {
+      base += seq.tiles * upt;
+      seq = seq_of(p, ++b);
+    }
+    s.b = b;
+    s.seq = seq;
+    s.in_seq = (at - base) / seq.tiles;
+    const int u0 = base + s.in_seq * seq.tiles;
+    s.j0 = at - u0;
+    s.j1 = min(end - u0, seq.tiles);
+    s.cta = (int)blockIdx.x;
+    s.whole = s.j0 == 0 && s.j1 == seq.tiles;
+    s.slot = 2 * s.cta + (s.j0 > 0 ? 0 : 1);
+    at = u0 + s.j1;
+    return true;
+  }
+};
+
+// The runs of a unit, for the kernel that joins them: run i is CTA cta0 + i's, its partial in slot(i).
+struct Runs {
+  int cta0, n;
+  bool aligned;
+  int per, u0;
+  __device__ __forceinline__ int slot(int i) const {
+    const int c = cta0 + i;
+    return 2 * c + (aligned || c * per > u0 ? 0 : 1);
+  }
+};
+
+__device__ __forceinline__ Runs runs_of(const Params& p, int lane, int grid, int b, int in_seq, const Seq& seq) {
+  const Split sp = split_of(p, lane, grid, false);
+  const int first = before(p, sp, lane, grid, b);
+  Runs r;
+  r.aligned = sp.aligned;
+  r.per = sp.per;
+  r.u0 = first + in_seq * seq.tiles;
+  if (sp.aligned) {
+    r.n = ctas_of(sp, seq.tiles, grid);
+    r.cta0 = first + in_seq * r.n;
+  } else {
+    r.cta0 = r.u0 / sp.per;
+    r.n = (r.u0 + seq.tiles - 1) / sp.per - r.cta0 + 1;
+  }
+  return r;
 }
 
 // Whether new token i sees slot s, a slot that some token may see.
@@ -167,6 +293,11 @@ __device__ __forceinline__ unsigned seen_by_any16(const Params& p, const Seq& q,
 }
 
 }  // namespace span
+
+// Whether the counts of the split fit their types.
+inline bool span_fits(const span::Params& p, long long units) {
+  return units * ((p.max_seq + span::kSpanTile - 1LL) / span::kSpanTile) <= 0x3fffffffLL && span_sms() <= 255;
+}
 
 // Launches a kernel that may be set up while the one before it on the stream runs (and waits for it with
 // griddepcontrol.wait before it reads anything).

@@ -87,12 +87,12 @@ template <bool TREE>
 struct Walk {
   const TcParams& p;
   int lane;
-  long long at, end, per;
-  span::Cursor cur;
+  long long at, end, per;  // prefill: items of this CTA
+  span::Walker runs;
 
   __device__ __forceinline__ Walk(const TcParams& prm, int ln, bool flag) : p(prm), lane(ln) {
     if constexpr (TREE) {
-      span::my_run(p.s, lane, flag, &at, &end, &per, &cur);
+      runs.begin(p.s, lane, flag);
     } else {
       if (flag)
         for (int b = lane; b < p.s.B; b += 32)
@@ -105,26 +105,20 @@ struct Walk {
 
   __device__ __forceinline__ bool next(Seg& s) {
     if constexpr (TREE) {
-      if (at >= end) return false;
-      const long long upt = (long long)p.s.Hkv * p.s.row_tiles;
-      while (at >= cur.seq_start + (long long)cur.seq.tiles * upt) {
-        cur.seq_start += (long long)cur.seq.tiles * upt;
-        cur.seq = span::seq_of(p.s, ++cur.b);
-      }
-      const long long in_seq = (at - cur.seq_start) / cur.seq.tiles;
-      const long long u0 = cur.seq_start + in_seq * cur.seq.tiles, u1 = u0 + cur.seq.tiles;
-      s.b = cur.b;
-      s.g = (int)(in_seq % p.s.Hkv);
-      s.L = cur.seq.L;
-      s.ctx = cur.seq.ctx;
-      s.n_b = cur.seq.n_b;
+      span::Piece pc;
+      if (!runs.next(p.s, pc)) return false;
+      s.b = pc.b;
+      s.g = pc.in_seq % p.s.Hkv;
+      s.L = pc.seq.L;
+      s.ctx = pc.seq.ctx;
+      s.n_b = pc.seq.n_b;
       s.sink_tiles = s.win_tile = 0;
-      s.j0 = (int)(at - u0);
-      s.j1 = (int)(min(end, u1) - u0);
-      s.row0 = (int)(in_seq / p.s.Hkv) * (p.pair ? 2 * kTcTile : kTcTile);
+      s.j0 = pc.j0;
+      s.j1 = pc.j1;
+      s.row0 = pc.in_seq / p.s.Hkv * (p.pair ? 2 * kTcTile : kTcTile);
       s.head0 = 0;
-      s.slot = (long long)cur.b * upt + in_seq + blockIdx.x;  // unit + CTA: grows along the list of tiles
-      at = u0 + s.j1;
+      // unit + CTA grows along the runs, so no two share it
+      s.slot = (long long)pc.b * p.s.Hkv * p.s.row_tiles + pc.in_seq + pc.cta;
       return true;
     } else {
       for (; at < end; at += per) {
@@ -601,32 +595,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 constexpr int kMergeCols = 2;  // column quads of a CTA
 __global__ void __launch_bounds__(kTcTile* kMergeCols) span_merge_kernel(const TcParams p, int grid_tc, int rows_per_unit) {
   const int lane = threadIdx.x & 31;
-  const long long upt = (long long)p.s.Hkv * p.s.row_tiles;
-  const long long unit = blockIdx.x;
-  const int b = (int)(unit / upt);
-  const long long in_seq = unit % upt;
-  ptx::pdl_wait();
+  const int upt = p.s.Hkv * p.s.row_tiles, unit = (int)blockIdx.x, b = unit / upt, in_seq = unit % upt;
+  // the lengths are the call's inputs: where the partials lie is found while the main kernel still runs
   const span::Seq sq = span::seq_of(p.s, b);
   if (sq.tiles == 0) return;
-  // where the unit's tiles lie in the list of all tiles
-  long long total, before;
-  span::count_tiles(p.s, lane, b, false, &total, &before);
-  const long long per = max(1LL, (total + grid_tc - 1) / grid_tc);
-  const long long u0 = before + in_seq * sq.tiles, u1 = u0 + sq.tiles;
-  const long long c0 = u0 / per, c1 = (u1 - 1) / per;
-  const int g = (int)(in_seq % p.s.Hkv), r0 = (int)(in_seq / p.s.Hkv) * rows_per_unit;
+  const span::Runs runs = span::runs_of(p.s, lane, grid_tc, b, in_seq, sq);
+  ptx::pdl_wait();
+  const int c0 = runs.cta0, c1 = runs.cta0 + runs.n - 1;
+  const int g = in_seq % p.s.Hkv, r0 = in_seq / p.s.Hkv * rows_per_unit;
   const int half = blockIdx.z;  // pair: which of the two row tiles
   const int m = threadIdx.x % kTcTile, q4 = (int)blockIdx.y * kMergeCols + threadIdx.x / kTcTile;
   const int row = r0 + half * kTcTile + m;
   if (row >= p.s.R || row % p.s.T >= sq.n_b) return;
   const int n_str = p.pair ? 1 : 2;  // partials of a row in one run
-  auto part = [&](long long c, int w) { return p.s.part + ((size_t)(unit + c) * 2 + (p.pair ? half : w)) * kPartFloats; };
+  auto part = [&](int c, int w) { return p.s.part + ((size_t)(unit + c) * 2 + (p.pair ? half : w)) * kPartFloats; };
   float M = -INFINITY;
-  for (long long c = c0; c <= c1; ++c)
+  for (int c = c0; c <= c1; ++c)
     for (int w = 0; w < n_str; ++w) M = fmaxf(M, __ldcg(part(c, w) + m));
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (long long c = c0; c <= c1; ++c)
+  for (int c = c0; c <= c1; ++c)
     for (int w = 0; w < n_str; ++w) {
       const float* pp = part(c, w);
       const float mc = __ldcg(pp + m);
@@ -683,6 +671,8 @@ cudaError_t launch_span_tc(const hata_dims_t& d, const span::Params& s, const Pa
   const long long kv_rows =
       pg ? ((long long)pg->n_blocks * d.n_kv_heads) << pg->block_shift : (long long)d.batch * d.n_kv_heads * d.max_seq;
   const long long q_rows = (long long)d.batch * d.n_q_heads * s.T;
+  const long long units = (long long)d.batch * d.n_kv_heads * p.s.row_tiles;
+  if (!span_fits(p.s, units)) return cudaErrorNotSupported;
   if (kv_rows + kTcTile > 0x7fffffffLL || q_rows + 2 * kTcTile > 0x7fffffffLL) return cudaErrorNotSupported;
   if (!make_bf16_rows_map(&qm, s.q, q_rows, kTcTile) || !make_bf16_rows_map(&km, s.K, kv_rows, p.box_rows) ||
       !make_bf16_rows_map(&vm, s.V, kv_rows, p.box_rows))
@@ -692,8 +682,6 @@ cudaError_t launch_span_tc(const hata_dims_t& d, const span::Params& s, const Pa
   if (pg) span_tc_kernel<true, true><<<sms, kTcThreads, kTcSmem, st>>>(qm, km, vm, p);
   else span_tc_kernel<true, false><<<sms, kTcThreads, kTcSmem, st>>>(qm, km, vm, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const long long units = (long long)d.batch * d.n_kv_heads * p.s.row_tiles;
-  if (units > 0x7fffffffLL) return cudaErrorNotSupported;
   return launch_early(span_merge_kernel, dim3((unsigned)units, kHeadDim / 4 / kMergeCols, p.pair ? 2 : 1),
                       kTcTile * kMergeCols, st, p, sms, rows);
 }
