@@ -29,8 +29,8 @@ using namespace span;
 constexpr int kSpThreads = 256;
 constexpr int kSpWarps = kSpThreads / 32;
 constexpr int kSpKeys = 16;  // slots of a warp in a tile
-// Registers of a thread: 256 x 224 of the SM's 65536 leave room for a CTA of the joining kernel (128 x 48), which is
-// then there, its prologue done, when the main kernel ends.
+// Registers of a thread: 256 x 224 of the SM's 65536 leave room for a CTA of the joining kernel (128 x 64), which is
+// then there, its prologue done, when the main kernel ends (measured at 240 registers, where it is not: 5 us later).
 constexpr int kSpRegs = 224;
 constexpr float kSpSlack = 8.f;  // log2 units
 static_assert(kSpWarps * kSpKeys == kSpanTile, "the warps share a tile");
@@ -147,11 +147,13 @@ __device__ __forceinline__ void finish_unit(const Params& p, float* sm_m, float*
   }
 }
 
-// Joins the partials of a unit in the order of the split: a warp per row, a lane per 4 columns.
-// grid = (units, ROWS / 4).
+// Joins the partials of a unit in the order of the split: a warp per row, a lane per 4 columns.  The partials were
+// just written by other SMs, so a round trip to them costs over a microsecond: eight rows of O are under way
+// before the weights are known.  grid = (units, ROWS / 4).
 constexpr int kJoinWarps = 4;
+constexpr int kJoinBatch = 8;
 template <typename T, int ROWS>
-__global__ void __launch_bounds__(kJoinWarps * 32) span_join_kernel(const Params p, int grid_main) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 8) span_join_kernel(const Params p, int grid_main) {
   const int lane = threadIdx.x & 31, r = (int)blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
   const int upt = p.Hkv * p.row_tiles, b = (int)blockIdx.x / upt, in_seq = (int)blockIdx.x % upt;
   const int g = in_seq % p.Hkv, row = in_seq / p.Hkv * ROWS + r;
@@ -162,8 +164,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) span_join_kernel(const Params
   const int n = runs.n;
   if (n == 1) return;  // written by the one CTA that had it
   ptx::pdl_wait();
+  float4 v[kJoinBatch];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k)
+      v[k] = i0 + k < n ? __ldcg(reinterpret_cast<const float4*>(part_of<ROWS>(p, runs.slot(i0 + k)) + 2 * ROWS) +
+                                 r * (kHeadDim / 4) + lane)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
   float M = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  fetch(0);
   for (int i0 = 0; i0 < n; i0 += 32) {  // 32 runs: a lane per run for the weights, then a lane per column for O
     float m = -INFINITY, li = 0.f;
     if (i0 + lane < n) {
@@ -186,16 +197,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) span_join_kernel(const Params
     o.z *= back;
     o.w *= back;
     M = m_new;
-    const int k1 = min(32, n - i0);
-#pragma unroll 8
-    for (int k = 0; k < k1; ++k) {
-      const float fk = __shfl_sync(0xffffffffu, f, k);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(part_of<ROWS>(p, runs.slot(i0 + k)) + 2 * ROWS) +
-                              r * (kHeadDim / 4) + lane);
-      o.x = fmaf(v.x, fk, o.x);
-      o.y = fmaf(v.y, fk, o.y);
-      o.z = fmaf(v.z, fk, o.z);
-      o.w = fmaf(v.w, fk, o.w);
+    for (int k0 = 0; k0 < 32 && i0 + k0 < n; k0 += kJoinBatch) {
+      if (i0 + k0 > 0) fetch(i0 + k0);
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k0 + k);  // 0 past the last run
+        o.x = fmaf(v[k].x, fk, o.x);
+        o.y = fmaf(v[k].y, fk, o.y);
+        o.z = fmaf(v[k].z, fk, o.z);
+        o.w = fmaf(v[k].w, fk, o.w);
+      }
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
