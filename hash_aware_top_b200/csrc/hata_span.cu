@@ -471,14 +471,13 @@ __global__ void __maxnreg__(kSpRegs) span_mma_kernel(const Params p) {
     for (int k = 0; k < kMmStages - 1; ++k) load(j0 + k);
     asm volatile("cp.async.wait_group %0;\n" ::"n"(kMmStages - 1) : "memory");
     __syncthreads();
-    uint32_t qa[MT][kHeadDim / 16][4];
+    // query fragments: 32 registers for 16 rows; with 32 rows, whose outputs take 128, they are read again each step
+    const uint32_t q_frag = sm_q + (uint32_t)((lane & 15) * kMmRowB + (((lane >> 4) ^ (lane & 7)) << 4));
+    uint32_t qa[kHeadDim / 16][4];
+    if constexpr (MT == 1) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-        const int r = lane & 15, c = 2 * ks + (lane >> 4);
-        ldsm_x4(qa[mt][ks], sm_q + (uint32_t)((16 * mt + r) * kMmRowB + ((c ^ (r & 7)) << 4)));
-      }
+      for (int ks = 0; ks < kHeadDim / 16; ++ks) ldsm_x4(qa[ks], q_frag ^ (uint32_t)(ks << 5));
+    }
     float o[MT][kHeadDim / 8][4];
     float m[MT][2], l[MT][2];
 #pragma unroll
@@ -512,8 +511,9 @@ __global__ void __maxnreg__(kSpRegs) span_mma_kernel(const Params p) {
         ldsm_x4(kb, kt ^ (uint32_t)(ks << 5));
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          mma16816(s[mt][0], qa[mt][ks], kb[0], kb[1]);
-          mma16816(s[mt][1], qa[mt][ks], kb[2], kb[3]);
+          if constexpr (MT > 1) ldsm_x4(qa[0], (q_frag ^ (uint32_t)(ks << 5)) + (uint32_t)(16 * mt * kMmRowB));
+          mma16816(s[mt][0], qa[MT > 1 ? 0 : ks], kb[0], kb[1]);
+          mma16816(s[mt][1], qa[MT > 1 ? 0 : ks], kb[2], kb[3]);
         }
       }
       const bool all_see = vis == 0xffffu && s0 + kSpKeys <= sq.ctx;
