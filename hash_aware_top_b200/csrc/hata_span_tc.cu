@@ -1,7 +1,7 @@
 // Attention on the 5th-generation tensor cores where many query rows share their keys: prefill with a
 // sliding window and sinks, and tree attention when a KV head has many (query head, token) rows.
 //
-// A CTA (ten warps, one per SM, persistent) runs two streams.  A stream is 128 query rows with their
+// A CTA (twelve warps, two idle; one per SM, persistent) runs two streams.  A stream is 128 query rows with their
 // own scores S and output O in TMEM (128 columns each) and a warpgroup whose thread owns one row:
 //   S = Q K^T (tcgen05.mma, M = N = 128)  ->  p = 2^(s c - m), c = scale log2 e, in registers  ->  P as bf16 over
 //   the first half of S  ->  O += P V (P from TMEM, V as an MN-major operand)
@@ -36,7 +36,11 @@ namespace {
 
 using span::Params;
 
-constexpr int kTcThreads = 320;
+constexpr int kTcThreads = 384;  // two warpgroups of rows, one of loader, MMA issue and two idle warps
+// Registers of a thread: 152 at launch, then 192 for the rows' warpgroups (a row's 128 scores stay in registers) and
+// 72 for the other (256 x 192 + 128 x 72 = 384 x 152); the rest of the SM's leaves room for a merging CTA.
+constexpr int kTcRegs = 152, kTcRowRegs = 192, kTcIssueRegs = 72;
+static_assert(256 * kTcRowRegs + 128 * kTcIssueRegs == kTcThreads * kTcRegs, "registers of the launch");
 constexpr int kTcMmaWarp = 8, kTcTmaWarp = 9;
 constexpr int kTcTile = 128;
 static_assert(kTcTile == span::kSpanTile, "the split of the work counts these tiles");
@@ -167,7 +171,7 @@ struct Bits128 {
 };
 
 template <bool TREE, bool PAGED>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __maxnreg__(kTcRegs)
     span_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const TcParams p) {
   extern __shared__ __align__(1024) unsigned char tc_smem[];
@@ -226,6 +230,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   Walk<TREE> walk(p, lane, blockIdx.x == 0 && warp == 0);
   Seg sg;
 
+  if (warp >= kTcMmaWarp) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kTcIssueRegs));
   if (warp == kTcTmaWarp) {
     // ---------------- loader: lane l issues box l ----------------
     uint32_t item = 0;  // ring items issued
@@ -375,8 +381,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc::mbar_wait(&drain, 0, kTcTries);
     }
     __syncwarp();
+  }
   } else {
     // ---------------- a stream's warpgroup: row m of its 128 ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kTcRowRegs));
     const int w = warp >> 2, m = tid & 127;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t sa = lane_base + (uint32_t)(w * kTcTile), oa = lane_base + 256u + (uint32_t)(w * kHeadDim);
@@ -591,8 +599,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-// Joins the partials of a unit: thread (row, 4 columns), partials in the order of the split.  grid = (units, 16).
-constexpr int kMergeCols = 2;  // column quads of a CTA
+// Joins the partials of a unit: thread (row, 4 columns), partials in the order of the split.
+// grid = (units, 32, row tiles of a unit).
+constexpr int kMergeCols = 1;  // column quads of a CTA
 __global__ void __launch_bounds__(kTcTile* kMergeCols) span_merge_kernel(const TcParams p, int grid_tc, int rows_per_unit) {
   const int lane = threadIdx.x & 31;
   const int upt = p.s.Hkv * p.s.row_tiles, unit = (int)blockIdx.x, b = unit / upt, in_seq = unit % upt;
