@@ -65,6 +65,67 @@ struct TcParams {
   int test_expire;
 };
 
+// Eight MMAs of K = 16 that make one 128 x 128 x 128 product, issued by one elected lane of a warp whose lanes all
+// call this together with the same arguments: descriptors then stay in uniform registers.  Issued under `if (lane ==
+// 0)` the same eight took 730 to 1050 cycles, against the 512 that the tensor core needs.
+// S = Q K^T: both operands K-major, four steps of 32 bytes in each half of 64 columns
+__device__ __forceinline__ void mma8_s(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b64 a, b;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+      "add.s64 a, %1, 1024;\n\tadd.s64 b, %2, 1024;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+      "add.s64 a, %1, 1026;\n\tadd.s64 b, %2, 1026;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+      "add.s64 a, %1, 1028;\n\tadd.s64 b, %2, 1028;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+      "add.s64 a, %1, 1030;\n\tadd.s64 b, %2, 1030;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}\n" ::"r"(d),
+      "l"(q), "l"(k), "r"(idesc)
+      : "memory");
+}
+// O (+)= P V: P in TMEM (8 columns per step), V MN-major (2048 bytes per step); `more`: add to O
+__device__ __forceinline__ void mma8_pv(uint32_t d, uint32_t pa, uint64_t v, uint32_t idesc, uint32_t more) {
+  asm volatile(
+      "{\n\t.reg .pred e, p;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "setp.eq.b32 p, 0, 0;\n\t"
+      "add.s32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+      "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+      "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+      "add.s32 a, %1, 32;\n\tadd.s64 b, %2, 512;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+      "add.s32 a, %1, 40;\n\tadd.s64 b, %2, 640;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+      "add.s32 a, %1, 48;\n\tadd.s64 b, %2, 768;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+      "add.s32 a, %1, 56;\n\tadd.s64 b, %2, 896;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t}\n" ::"r"(d),
+      "r"(pa), "l"(v), "r"(idesc), "r"(more)
+      : "memory");
+}
+// tc::commit by the lane that issues the MMAs
+__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(tc::smem_u32(bar))
+      : "memory");
+}
+
 // One CTA's next piece of work: a run of key tiles for its two streams.
 struct Seg {
   int b, g;
@@ -305,7 +366,7 @@ __global__ void __maxnreg__(kTcRegs)
       tc::mbar_wait(&full[it % kTcStages], (it / kTcStages) & 1, kTcTries);
     if (n_q > 0) tc::mbar_wait(&q_full, (n_q - 1) & 1, kTcTries);
   } else if (warp == kTcMmaWarp) {
-    // ---------------- MMA issue ----------------
+    // ---------------- MMA issue: every lane runs this, one elected lane issues ----------------
     bool ok = true;
     if (p.test_expire && !tc::mbar_wait(&never, 0, kTcTestTries)) {  // test hook: this wait runs out
       if (lane == 0) set_status(p.s.status, HATA_ERR_TIMEOUT);
@@ -314,72 +375,63 @@ __global__ void __maxnreg__(kTcRegs)
     }
     constexpr uint32_t idS = tc::idesc_bf16(kTcTile, kTcTile, false);
     constexpr uint32_t idPV = tc::idesc_bf16(kTcTile, kHeadDim, true);
-    uint32_t item0 = 0;       // first ring item of the run
-    uint32_t done[2] = {0, 0};  // tiles whose P this stream has delivered
+    uint32_t item0 = 0;         // first ring item of the run
+    uint32_t done0 = 0, done1 = 0;  // tiles whose P the streams have delivered
     for (int n_seg = 0; ok && walk.next(sg); ++n_seg) {
-      const int n = sg.j1 - sg.j0, steps = steps_of(n);
-      if (lane == 0) {
-        ok = wait_ok(&q_full, (uint32_t)(n_seg & 1));
-        auto wait_item = [&](int k) {
-          const uint32_t it = item0 + (uint32_t)k;
-          return wait_ok(&full[it % kTcStages], (it / kTcStages) & 1);
-        };
-        auto stage_of = [&](int k) { return base + kTcRing + ((item0 + (uint32_t)k) % kTcStages) * kTcTileB; };
-        auto free_item = [&](int k) { tc::commit(&freed[(item0 + (uint32_t)k) % kTcStages]); };
-        auto issue_s = [&](int i, int w) {
-          tc::fence_after();
-          const uint32_t qb = base + kTcQ + (pair ? (uint32_t)w * kTcTileB : 0u), kb = stage_of(item_k(i, w));
-#pragma unroll
-          for (int ks = 0; ks < kHeadDim / 16; ++ks) {
-            const uint32_t off = (uint32_t)((ks >> 2) * (kTcTileB / 2) + (ks & 3) * 32);
-            tc::mma(tmem + (uint32_t)w * kTcTile, tc::desc_kmajor_sw128(qb + off), tc::desc_kmajor_sw128(kb + off), idS,
-                    ks > 0 ? 1u : 0u);
-          }
-          tc::commit(&s_full[w]);
-        };
-        auto issue_pv = [&](int i, int w) {
-          tc::fence_after();
-          const uint32_t vb = stage_of(item_v(n, i, w));
-#pragma unroll
-          for (int ks = 0; ks < kTcTile / 16; ++ks)
-            tc::mma_ts(tmem + 256u + (uint32_t)w * kHeadDim, tmem + (uint32_t)(w * kTcTile + ks * 8),
-                       tc::desc_mnmajor_sw128(vb + (uint32_t)ks * 2048u, (uint32_t)(kTcTileB / 2)), idPV,
-                       (i > 0 || ks > 0) ? 1u : 0u);
-        };
-        const int s0n = pair ? 2 : streams_in(n, 0);  // streams of the first step
-        for (int w = 0; ok && w < s0n; ++w) {
-          if ((!pair || w == 0) && !(ok = wait_item(item_k(0, w)))) break;
-          issue_s(0, w);
-          if (!pair || w == 1) free_item(item_k(0, w));
-        }
-        if (ok && steps == 1) tc::commit(&q_free);
-        for (int i = 0; ok && i < steps; ++i) {
-          const int m = pair ? 2 : streams_in(n, i);
-          const int m_next = i + 1 < steps ? (pair ? 2 : streams_in(n, i + 1)) : 0;
-          for (int w = 0; ok && w < m; ++w) {
-            if (!(ok = wait_ok(&p_full[w], done[w] & 1))) break;
-            ++done[w];
-            if ((!pair || w == 0) && !(ok = wait_item(item_v(n, i, w)))) break;
-            issue_pv(i, w);
-            if (!pair || w == 1) free_item(item_v(n, i, w));
-            if (w < m_next) {
-              if ((!pair || w == 0) && !(ok = wait_item(item_k(i + 1, w)))) break;
-              issue_s(i + 1, w);
-              if (!pair || w == 1) free_item(item_k(i + 1, w));
-              if (i + 2 == steps && w == m_next - 1) tc::commit(&q_free);
-            } else {
-              tc::commit(&o_full[w]);  // the stream's last PV
-            }
-          }
-        }
-        item0 += (uint32_t)(2 * n);
+      const int n = __shfl_sync(0xffffffffu, sg.j1 - sg.j0, 0), steps = steps_of(n);
+      ok = wait_warp(&q_full, (uint32_t)(n_seg & 1));
+      auto wait_item = [&](int k) {
+        const uint32_t it = item0 + (uint32_t)k;
+        return wait_warp(&full[it % kTcStages], (it / kTcStages) & 1);
+      };
+      auto stage_of = [&](int k) { return base + kTcRing + ((item0 + (uint32_t)k) % kTcStages) * kTcTileB; };
+      auto free_item = [&](int k) { commit_elected(&freed[(item0 + (uint32_t)k) % kTcStages]); };
+      auto issue_s = [&](int i, int w) {
+        tc::fence_after();
+        mma8_s(tmem + (uint32_t)w * kTcTile, tc::desc_kmajor_sw128(base + kTcQ + (pair ? (uint32_t)w * kTcTileB : 0u)),
+               tc::desc_kmajor_sw128(stage_of(item_k(i, w))), idS);
+        commit_elected(&s_full[w]);
+      };
+      auto issue_pv = [&](int i, int w) {
+        tc::fence_after();
+        mma8_pv(tmem + 256u + (uint32_t)w * kHeadDim, tmem + (uint32_t)(w * kTcTile),
+                tc::desc_mnmajor_sw128(stage_of(item_v(n, i, w)), (uint32_t)(kTcTileB / 2)), idPV, i > 0 ? 1u : 0u);
+      };
+      const int s0n = pair ? 2 : streams_in(n, 0);  // streams of the first step
+#pragma unroll 1
+      for (int w = 0; ok && w < s0n; ++w) {
+        if ((!pair || w == 0) && !(ok = wait_item(item_k(0, w)))) break;
+        issue_s(0, w);
+        if (!pair || w == 1) free_item(item_k(0, w));
       }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      if (ok && steps == 1) commit_elected(&q_free);
+#pragma unroll 1
+      for (int i = 0; ok && i < steps; ++i) {
+        const int m = pair ? 2 : streams_in(n, i);
+        const int m_next = i + 1 < steps ? (pair ? 2 : streams_in(n, i + 1)) : 0;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (!ok || w >= m) break;
+          uint32_t& done = w ? done1 : done0;
+          if ((!pair || w == 0) && !(ok = wait_item(item_v(n, i, w)))) break;
+          if (!(ok = wait_warp(&p_full[w], done & 1))) break;
+          ++done;
+          issue_pv(i, w);
+          if (!pair || w == 1) free_item(item_v(n, i, w));
+          if (w < m_next) {
+            if ((!pair || w == 0) && !(ok = wait_item(item_k(i + 1, w)))) break;
+            issue_s(i + 1, w);
+            if (!pair || w == 1) free_item(item_k(i + 1, w));
+            if (i + 2 == steps && w == m_next - 1) commit_elected(&q_free);
+          } else {
+            commit_elected(&o_full[w]);  // the stream's last PV
+          }
+        }
+      }
+      item0 += (uint32_t)(2 * n);
     }
-    if (lane == 0) {
-      tc::commit(&drain);  // every MMA issued above completes before the CTA leaves
-      tc::mbar_wait(&drain, 0, kTcTries);
-    }
+    commit_elected(&drain);  // every MMA issued above completes before the CTA leaves
+    tc::mbar_wait(&drain, 0, kTcTries);
     __syncwarp();
   }
   } else {
