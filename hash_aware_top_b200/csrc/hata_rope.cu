@@ -13,6 +13,8 @@
 // of 16 bytes, so the mean square is a shuffle tree and the partner of a half-split pair lies rot / 2
 // elements, a whole number of lanes, away.  The 8 warps of a CTA take 8 consecutive tokens and the same rows of
 // each, so that the scattered stores of neighbouring tokens meet in L2 as 2 KB runs per head.
+#include <algorithm>
+
 #include "hata_kernels.cuh"
 
 namespace hata {
@@ -21,6 +23,7 @@ namespace {
 
 constexpr int kRopeWarps = 8;
 constexpr int kRopeBatch = 4;  // row steps whose loads are in flight together
+constexpr int kRopeCtas = 3;   // per SM: 80 registers a thread
 
 struct RopeParams {
   const void *q_in, *k_in, *v_in;
@@ -77,7 +80,7 @@ __device__ __forceinline__ uint4 Vec16<__nv_bfloat16>::pack(const float (&x)[8])
 }
 
 template <typename T, bool INTER, bool PAGED>
-__global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) norm_rope_kernel(const RopeParams p) {
   constexpr int N = Vec16<T>::N;           // elements of a lane's vector
   constexpr int LANES = kHeadDim / N;      // lanes of a row
   constexpr int RPS = 32 / LANES;          // rows of one warp step
@@ -144,20 +147,22 @@ __global__ void __launch_bounds__(kRopeWarps * 32) norm_rope_kernel(const RopePa
   const T* v = static_cast<const T*>(p.v_in) + tok * (size_t)p.v_stride + e0;
   const int first = sp * p.steps_per_warp * RPS;
   const int last = min(rows, first + p.steps_per_warp * RPS);
-  for (int r0 = first; r0 < last; r0 += kRopeBatch * RPS) {
-    uint4 in[kRopeBatch];
+  auto load = [&](int r0, uint4 (&v4)[kRopeBatch]) {
 #pragma unroll
     for (int u = 0; u < kRopeBatch; ++u) {
       const int r = r0 + u * RPS + sub;
-      if (r < last) {
-        const T* src = r < p.Hq ? q + (size_t)r * kHeadDim
-                                : r < p.Hq + p.Hkv ? kk + (size_t)(r - p.Hq) * kHeadDim
-                                                   : v + (size_t)(r - p.Hq - p.Hkv) * kHeadDim;
-        in[u] = __ldg(reinterpret_cast<const uint4*>(src));
-      } else {
-        in[u] = make_uint4(0u, 0u, 0u, 0u);
-      }
+      const T* src = r < p.Hq ? q + (size_t)r * kHeadDim
+                              : r < p.Hq + p.Hkv ? kk + (size_t)(r - p.Hq) * kHeadDim
+                                                 : v + (size_t)(r - p.Hq - p.Hkv) * kHeadDim;
+      v4[u] = r < last ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
     }
+  };
+  uint4 in[kRopeBatch], nx[kRopeBatch];
+  load(first, nx);
+  for (int r0 = first; r0 < last; r0 += kRopeBatch * RPS) {
+#pragma unroll
+    for (int u = 0; u < kRopeBatch; ++u) in[u] = nx[u];
+    load(r0 + kRopeBatch * RPS, nx);  // the next rows are under way while these are turned
 #pragma unroll
     for (int u = 0; u < kRopeBatch; ++u) {
       const int r = r0 + u * RPS + sub;
@@ -269,7 +274,11 @@ cudaError_t launch_norm_rope(const hata_dims_t& d, const RopeArgs& a, const Page
   const int rps = d.dtype == HATA_BF16 ? 2 : 1;
   const int steps = (p.Hq + 2 * p.Hkv + rps - 1) / rps;
   p.tok_blocks = (p.n_tok + kRopeWarps - 1) / kRopeWarps;
-  p.n_split = (steps + kRopeBatch - 1) / kRopeBatch;
+  // A warp takes a whole token, so that positions, table and weights are fetched once for all its rows, unless
+  // the tokens are too few to fill the SMs twice; then several warps share one, down to a batch of rows each.
+  const long long fill = 2LL * kRopeCtas * kRopeWarps * span_sms(), tokens = (long long)d.batch * p.n_tok;
+  const int most = (steps + kRopeBatch - 1) / kRopeBatch;
+  p.n_split = (int)std::min<long long>(most, std::max<long long>(1, fill / tokens));
   p.steps_per_warp = (steps + p.n_split - 1) / p.n_split;
   const long long gx = (long long)p.tok_blocks * p.n_split;
   if (gx > 0x7fffffffLL || d.batch > 65535) return cudaErrorNotSupported;

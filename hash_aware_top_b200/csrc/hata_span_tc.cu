@@ -6,7 +6,7 @@
 //   S = Q K^T (tcgen05.mma, M = N = 128)  ->  p = 2^(s c - m), c = scale log2 e, in registers  ->  P as bf16 over
 //   the first half of S  ->  O += P V (P from TMEM, V as an MN-major operand)
 // While one stream's warpgroup computes its exponentials, the tensor core works for the other.  K and V tiles of
-// 128 slots come through one ring of five 32 KB stages (TMA; a page of fewer than 128 slots is a box of its own);
+// 128 slots come through one ring of five 32 KB stages (four for a prefill) (TMA; a page of fewer than 128 slots is a box of its own);
 // one warp loads, one lane of another issues the MMAs.  The running maximum m moves only when a row's maximum
 // passes it by more than 2^8; O is then rescaled in TMEM, which is safe once S has arrived, since the MMAs run in
 // order and PV of the tile before was issued first.
@@ -45,10 +45,11 @@ constexpr int kTcMmaWarp = 8, kTcTmaWarp = 9;
 constexpr int kTcTile = 128;
 static_assert(kTcTile == span::kSpanTile, "the split of the work counts these tiles");
 constexpr int kTcTileB = kTcTile * kHeadDim * 2;  // 32 KB
-constexpr int kTcStages = 5;
+constexpr int kTcStages = 5;  // of the ring; a prefill uses the last one to write its rows out
 constexpr uint32_t kTcQ = 0;                      // two tiles of query rows
 constexpr uint32_t kTcRing = 2 * kTcTileB;
-constexpr int kTcSmem = (2 + kTcStages) * kTcTileB + 1024;  // + alignment to 1024 bytes
+constexpr uint32_t kTcOut = kTcRing + (kTcStages - 1) * kTcTileB;  // per stream 128 rows x 64 columns of output, 16 KB
+constexpr int kTcSmem = (2 + kTcStages) * kTcTileB + 1024;         // + alignment to 1024 bytes
 constexpr uint32_t kTcTmemCols = 512;             // S of the streams at 0 and 128, O at 256 and 384
 constexpr uint32_t kTcTries = 1u << 22, kTcTestTries = 1u << 10;
 constexpr float kTcSlack = 8.f;  // log2 units: p <= 2^8 between rescales
@@ -58,14 +59,16 @@ struct TcParams {
   Params s;
   int prefill_heads;  // P: heads of a prefill CTA
   int pos_block;      // prefill: positions of a CTA (256 / P)
+  int pos_shift;      // prefill: log2 of the rows of one head in a stream
   int n_blocks_pos;   // prefill: blocks of positions
+  int rows_of_items;  // prefill: CTAs' items per block of positions, B * Hq / P
   int pair;           // tree: two tiles of rows (else one, its key tiles shared out)
   int box_rows;       // rows of a K / V box
   int q_box;          // rows of a Q box
   int test_expire;
 };
 
-// Eight MMAs of K = 16 that make one 128 x 128 x 128 product, issued by one elected lane of a warp whose lanes all
+// The MMAs of K = 16 that make one 128 x 128 x 128 product, issued by one elected lane of a warp whose lanes all
 // call this together with the same arguments: descriptors then stay in uniform registers.  Issued under `if (lane ==
 // 0)` the same eight took 730 to 1050 cycles, against the 512 that the tensor core needs.
 // S = Q K^T: both operands K-major, four steps of 32 bytes in each half of 64 columns
@@ -93,8 +96,8 @@ __device__ __forceinline__ void mma8_s(uint32_t d, uint64_t q, uint64_t k, uint3
       "l"(q), "l"(k), "r"(idesc)
       : "memory");
 }
-// O (+)= P V: P in TMEM (8 columns per step), V MN-major (2048 bytes per step); `more`: add to O
-__device__ __forceinline__ void mma8_pv(uint32_t d, uint32_t pa, uint64_t v, uint32_t idesc, uint32_t more) {
+// Half of O (+)= P V, 64 slots: P in TMEM (8 columns per step), V MN-major (2048 bytes per step); `more`: add to O
+__device__ __forceinline__ void mma4_pv(uint32_t d, uint32_t pa, uint64_t v, uint32_t idesc, uint32_t more) {
   asm volatile(
       "{\n\t.reg .pred e, p;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
@@ -106,14 +109,6 @@ __device__ __forceinline__ void mma8_pv(uint32_t d, uint32_t pa, uint64_t v, uin
       "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
       "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
-      "add.s32 a, %1, 32;\n\tadd.s64 b, %2, 512;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
-      "add.s32 a, %1, 40;\n\tadd.s64 b, %2, 640;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
-      "add.s32 a, %1, 48;\n\tadd.s64 b, %2, 768;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
-      "add.s32 a, %1, 56;\n\tadd.s64 b, %2, 896;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t}\n" ::"r"(d),
       "r"(pa), "l"(v), "r"(idesc), "r"(more)
       : "memory");
@@ -142,6 +137,39 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+// 16 consecutive 32-bit columns written to this thread's TMEM lane
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};\n" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -152,7 +180,7 @@ template <bool TREE>
 struct Walk {
   const TcParams& p;
   int lane;
-  long long at, end, per;  // prefill: items of this CTA
+  int at, end, per;  // prefill: items of this CTA
   span::Walker runs;
 
   __device__ __forceinline__ Walk(const TcParams& prm, int ln, bool flag) : p(prm), lane(ln) {
@@ -164,7 +192,7 @@ struct Walk {
           if (p.s.seq_lens[b] > p.s.max_seq) set_status(p.s.status, HATA_ERR_INVALID_ARG);
       per = gridDim.x;
       at = blockIdx.x;
-      end = (long long)p.n_blocks_pos * p.s.B * (p.s.Hq / p.prefill_heads);
+      end = p.n_blocks_pos * p.rows_of_items;
     }
   }
 
@@ -187,9 +215,9 @@ struct Walk {
       return true;
     } else {
       for (; at < end; at += per) {
-        const int hb = p.s.Hq / p.prefill_heads;
-        const long long rest = at % ((long long)p.s.B * hb);
-        const int blk = p.n_blocks_pos - 1 - (int)(at / ((long long)p.s.B * hb));  // the longest rows first
+        const unsigned blk_up = (unsigned)at / (unsigned)p.rows_of_items, rest = (unsigned)at % (unsigned)p.rows_of_items;
+        const unsigned hb = (unsigned)(p.rows_of_items / p.s.B);
+        const int blk = p.n_blocks_pos - 1 - (int)blk_up;  // the longest rows first
         s.b = (int)(rest / hb);
         s.head0 = (int)(rest % hb) * p.prefill_heads;
         s.g = s.head0 / p.s.G;
@@ -235,9 +263,10 @@ template <bool TREE, bool PAGED>
 __global__ void __maxnreg__(kTcRegs)
     span_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const TcParams p) {
+  constexpr uint32_t kStages = TREE ? kTcStages : kTcStages - 1;
   extern __shared__ __align__(1024) unsigned char tc_smem[];
-  __shared__ __align__(8) uint64_t q_full, q_free, full[kTcStages], freed[kTcStages], s_full[2], p_full[2], o_full[2],
-      drain, never;
+  __shared__ __align__(8) uint64_t q_full, q_free, full[kStages], freed[kStages], s_full[2], p_half[2], p_full[2],
+      o_full[2], drain, never;
   __shared__ uint32_t tmem_s;
   __shared__ volatile int abort_s;
 
@@ -247,12 +276,13 @@ __global__ void __maxnreg__(kTcRegs)
   if (tid == 256) {
     tc::mbar_init(&q_full, 1);
     tc::mbar_init(&q_free, 1);
-    for (int i = 0; i < kTcStages; ++i) {
+    for (uint32_t i = 0; i < kStages; ++i) {
       tc::mbar_init(&full[i], 1);
       tc::mbar_init(&freed[i], 1);
     }
     for (int w = 0; w < 2; ++w) {
       tc::mbar_init(&s_full[w], 1);
+      tc::mbar_init(&p_half[w], kTcTile);
       tc::mbar_init(&p_full[w], kTcTile);
       tc::mbar_init(&o_full[w], 1);
     }
@@ -324,7 +354,7 @@ __global__ void __maxnreg__(kTcRegs)
         }
       }
       auto load = [&](const CUtensorMap* map, int tile) -> bool {  // the next ring item
-        const uint32_t st = item % kTcStages, round = item / kTcStages;
+        const uint32_t st = item % kStages, round = item / kStages;
         if (round > 0 && !wait_warp(&freed[st], (round - 1) & 1)) return false;
         const uint32_t dst = base + kTcRing + st * kTcTileB;
         const int s0 = tile * kTcTile;
@@ -362,8 +392,8 @@ __global__ void __maxnreg__(kTcRegs)
       }
     }
     // every copy still in flight lands before the CTA leaves
-    for (uint32_t it = item > kTcStages ? item - kTcStages : 0; it < item; ++it)
-      tc::mbar_wait(&full[it % kTcStages], (it / kTcStages) & 1, kTcTries);
+    for (uint32_t it = item > kStages ? item - kStages : 0; it < item; ++it)
+      tc::mbar_wait(&full[it % kStages], (it / kStages) & 1, kTcTries);
     if (n_q > 0) tc::mbar_wait(&q_full, (n_q - 1) & 1, kTcTries);
   } else if (warp == kTcMmaWarp) {
     // ---------------- MMA issue: every lane runs this, one elected lane issues ----------------
@@ -382,20 +412,21 @@ __global__ void __maxnreg__(kTcRegs)
       ok = wait_warp(&q_full, (uint32_t)(n_seg & 1));
       auto wait_item = [&](int k) {
         const uint32_t it = item0 + (uint32_t)k;
-        return wait_warp(&full[it % kTcStages], (it / kTcStages) & 1);
+        return wait_warp(&full[it % kStages], (it / kStages) & 1);
       };
-      auto stage_of = [&](int k) { return base + kTcRing + ((item0 + (uint32_t)k) % kTcStages) * kTcTileB; };
-      auto free_item = [&](int k) { commit_elected(&freed[(item0 + (uint32_t)k) % kTcStages]); };
+      auto stage_of = [&](int k) { return base + kTcRing + ((item0 + (uint32_t)k) % kStages) * kTcTileB; };
+      auto free_item = [&](int k) { commit_elected(&freed[(item0 + (uint32_t)k) % kStages]); };
       auto issue_s = [&](int i, int w) {
         tc::fence_after();
         mma8_s(tmem + (uint32_t)w * kTcTile, tc::desc_kmajor_sw128(base + kTcQ + (pair ? (uint32_t)w * kTcTileB : 0u)),
                tc::desc_kmajor_sw128(stage_of(item_k(i, w))), idS);
         commit_elected(&s_full[w]);
       };
-      auto issue_pv = [&](int i, int w) {
+      auto issue_pv = [&](int i, int w, int half) {
         tc::fence_after();
-        mma8_pv(tmem + 256u + (uint32_t)w * kHeadDim, tmem + (uint32_t)(w * kTcTile),
-                tc::desc_mnmajor_sw128(stage_of(item_v(n, i, w)), (uint32_t)(kTcTileB / 2)), idPV, i > 0 ? 1u : 0u);
+        mma4_pv(tmem + 256u + (uint32_t)w * kHeadDim, tmem + (uint32_t)(w * kTcTile + half * 32),
+                tc::desc_mnmajor_sw128(stage_of(item_v(n, i, w)) + (uint32_t)half * 8192u, (uint32_t)(kTcTileB / 2)),
+                idPV, (i > 0 || half) ? 1u : 0u);
       };
       const int s0n = pair ? 2 : streams_in(n, 0);  // streams of the first step
 #pragma unroll 1
@@ -414,9 +445,11 @@ __global__ void __maxnreg__(kTcRegs)
           if (!ok || w >= m) break;
           uint32_t& done = w ? done1 : done0;
           if ((!pair || w == 0) && !(ok = wait_item(item_v(n, i, w)))) break;
+          if (!(ok = wait_warp(&p_half[w], done & 1))) break;
+          issue_pv(i, w, 0);
           if (!(ok = wait_warp(&p_full[w], done & 1))) break;
           ++done;
-          issue_pv(i, w);
+          issue_pv(i, w, 1);
           if (!pair || w == 1) free_item(item_v(n, i, w));
           if (w < m_next) {
             if ((!pair || w == 0) && !(ok = wait_item(item_k(i + 1, w)))) break;
@@ -447,7 +480,7 @@ __global__ void __maxnreg__(kTcRegs)
       const int n = sg.j1 - sg.j0, steps = steps_of(n);
       const int mine = pair ? steps : (n + 1 - w) / 2;  // steps of this stream
       // what this row sees
-      int t = 0, row = 0;
+      int t = 0, row = 0, t_lo = 0, t_hi = 0;
       bool live;
       Bits128 seen{0u, 0u, 0u, 0u}, any{0u, 0u, 0u, 0u};
       const bool has_new = TREE && sg.j1 * kTcTile > sg.ctx;  // the run reaches the new tokens
@@ -487,8 +520,11 @@ __global__ void __maxnreg__(kTcRegs)
           any.w3 = __reduce_or_sync(0xffffffffu, p.s.mask ? any.w3 : 0xffffffffu) & span::low_bits(sg.n_b - 96);
         }
       } else {
-        t = p.prefill_heads == 1 ? sg.row0 + w * kTcTile + m : sg.row0 + m % p.pos_block;
+        t = p.prefill_heads == 1 ? sg.row0 + w * kTcTile + m : sg.row0 + (m & (p.q_box - 1));
         live = t < sg.L;
+        // the stream's positions, for the test whether a tile lies at an edge of what they see
+        t_lo = p.prefill_heads == 1 ? sg.row0 + w * kTcTile : sg.row0;
+        t_hi = t_lo + min(p.pos_block, kTcTile) - 1;
       }
       float m_used = -INFINITY, l = 0.f;
       for (int i = 0; i < mine; ++i) {
@@ -500,37 +536,49 @@ __global__ void __maxnreg__(kTcRegs)
 #pragma unroll
         for (int k = 0; k < 4; ++k) tc::ld32_nowait(sa + 32 * k, x[k]);
         tc::ld_wait();
+        // Tiles at an edge of what the rows see: visibility words of this row, 32 slots each.  Chunks that every row of
+        // the warp sees need no masking, and those that none sees (bit k of `none`) no exponentials.
         const uint32_t ninf = 0xff800000u;
+        unsigned none = 0;
+        bool edge;
         if constexpr (TREE) {
-          if (s0 + kTcTile > sg.ctx) {
+          edge = s0 + kTcTile > sg.ctx;
+        } else {
+          edge = s0 + kTcTile > t_lo + 1 || (s0 <= t_hi - p.s.window && s0 + kTcTile > p.s.sink);
+        }
+        if (edge) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t v = seen.at(s0 + 32 * k - sg.ctx);
+          for (int k = 0; k < 4; ++k) {
+            uint32_t v;
+            if constexpr (TREE) {
+              v = seen.at(s0 + 32 * k - sg.ctx);
+            } else {
+              const int e0 = s0 + 32 * k;
+              v = span::low_bits(t + 1 - e0) &
+                  (~span::low_bits(t - min(p.s.window, t + 1) + 1 - e0) | span::low_bits(min(p.s.sink, sg.L) - e0));
+            }
+            if (!__any_sync(0xffffffffu, v != 0u)) none |= 1u << k;
+            if (__any_sync(0xffffffffu, v != 0xffffffffu)) {
 #pragma unroll
               for (int e = 0; e < 32; ++e) x[k][e] = (v >> e) & 1u ? x[k][e] : ninf;
             }
           }
-        } else {
-          // visible: e <= hi and (e >= lo or e < sk)
-          const int hi = t - s0, lo = t - min(p.s.window, t + 1) + 1 - s0, sk = min(p.s.sink, sg.L) - s0;
-          if (__any_sync(0xffffffffu, hi < kTcTile - 1 || (lo > 0 && sk < kTcTile))) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const int ee = 32 * k + e;
-                x[k][e] = (ee <= hi && (ee >= lo || ee < sk)) ? x[k][e] : ninf;
-              }
-          }
         }
-        float mx[4];
+        float mx;
+        {
+          float m8[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          mx[k] = __uint_as_float(x[k][0]);
+          for (int h = 0; h < 8; ++h) m8[h] = fmax3(__uint_as_float(x[0][h]), __uint_as_float(x[0][h + 8]), __uint_as_float(x[0][h + 16]));
 #pragma unroll
-          for (int e = 1; e < 32; ++e) mx[k] = fmaxf(mx[k], __uint_as_float(x[k][e]));
+          for (int e = 24; e < 120; e += 16)
+#pragma unroll
+            for (int h = 0; h < 8; ++h)
+              m8[h] = fmax3(m8[h], __uint_as_float(x[(e + h) >> 5][(e + h) & 31]), __uint_as_float(x[(e + 8 + h) >> 5][(e + 8 + h) & 31]));
+#pragma unroll
+          for (int h = 0; h < 8; ++h) m8[h] = fmaxf(m8[h], __uint_as_float(x[3][24 + h]));
+          mx = fmaxf(fmax3(m8[0], m8[1], m8[2]), fmax3(fmax3(m8[3], m8[4], m8[5]), m8[6], m8[7]));
         }
-        const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        const float m_tile = mx * c;
         if (i == 0) {
           m_used = m_tile;
         } else if (__any_sync(0xffffffffu, m_tile > m_used + kTcSlack)) {
@@ -547,41 +595,18 @@ __global__ void __maxnreg__(kTcRegs)
           l *= alpha;
           m_used = m_new;
         }
-        const float mr = m_used == -INFINITY ? 0.f : m_used;  // nothing seen yet: p = 2^-inf = 0
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float pr = ex2(fmaf(__uint_as_float(x[k][e]), c, -mr));
-            sum[e & 3] += pr;
-            x[k][e] = __float_as_uint(pr);
-          }
-        }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            pk[e] = bf16x2(__uint_as_float(x[2 * k][2 * e]), __uint_as_float(x[2 * k][2 * e + 1]));
-            pk[16 + e] = bf16x2(__uint_as_float(x[2 * k + 1][2 * e]), __uint_as_float(x[2 * k + 1][2 * e + 1]));
-          }
-          tc::st32(sa + 32 * k, pk);
-        }
-        tc::st_wait();
         // value rows that nobody sees (possibly not finite) are zeroed, so that 0 * V stays 0; in a pair the
         // first stream does it for both, since its PV is issued first
         if ((!pair || w == 0) && s0 + kTcTile > sg.ctx) {
           const uint32_t it = item0 + (uint32_t)item_v(n, i, w);
-          if (!(ok = wait_warp(&full[it % kTcStages], (it / kTcStages) & 1))) break;
+          if (!(ok = wait_warp(&full[it % kStages], (it / kStages) & 1))) break;
           bool drop = s0 + m >= sg.L;
           if constexpr (TREE) {
             const int j = s0 + m - sg.ctx;
             if (!drop && j >= 0) drop = !(any.at(j) & 1u);
           }
           if (drop) {
-            unsigned char* vrow = tc_smem + (base - tc::smem_u32(tc_smem)) + kTcRing + (it % kTcStages) * kTcTileB +
+            unsigned char* vrow = tc_smem + (base - tc::smem_u32(tc_smem)) + kTcRing + (it % kStages) * kTcTileB +
                                   (m >> 3) * 1024 + (m & 7) * 128;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -591,6 +616,60 @@ __global__ void __maxnreg__(kTcRegs)
           }
           tc::fence_async_smem();
         }
+        // p = 2^(x c - m) and its sum, two at a time; each half of P is handed over as soon as it is stored, so that
+        // its PV runs while the other half is computed
+        const float mr = m_used == -INFINITY ? 0.f : m_used;  // nothing seen yet: p = 2^-inf = 0
+        const uint64_t c2 = pack2(c, c), mr2 = pack2(-mr, -mr);
+        uint64_t sum2[2] = {0ull, 0ull};
+        auto chunk = [&](int k, uint32_t (&pk)[16]) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float a, d;
+            unpack2(fma2(pack2(__uint_as_float(x[k][2 * e]), __uint_as_float(x[k][2 * e + 1])), c2, mr2), a, d);
+            a = ex2(a);
+            d = ex2(d);
+            sum2[e & 1] = add2(sum2[e & 1], pack2(a, d));
+            pk[e] = bf16x2(a, d);
+          }
+        };
+        if (none == 0) {
+          uint32_t pk[4][16];
+          chunk(0, pk[0]);
+          st16(sa, pk[0]);
+          chunk(1, pk[1]);
+          st16(sa + 16, pk[1]);
+          chunk(2, pk[2]);
+          tc::st_wait();  // the stores of chunks 0 and 1 are done by now
+          tc::fence_before();
+          tc::mbar_arrive(&p_half[w]);
+          st16(sa + 32, pk[2]);
+          chunk(3, pk[3]);
+          st16(sa + 48, pk[3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t pk[16];
+            if ((none >> k) & 1u) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = 0u;
+            } else {
+              chunk(k, pk);
+            }
+            st16(sa + 16 * k, pk);
+            if (k == 1) {
+              tc::st_wait();
+              tc::fence_before();
+              tc::mbar_arrive(&p_half[w]);
+            }
+          }
+        }
+        {
+          float a, d, e, f;
+          unpack2(sum2[0], a, d);
+          unpack2(sum2[1], e, f);
+          l += (a + d) + (e + f);
+        }
+        tc::st_wait();
         tc::fence_before();
         tc::mbar_arrive(&p_full[w]);
       }
@@ -619,24 +698,39 @@ __global__ void __maxnreg__(kTcRegs)
           }
         }
       } else {
-        const int head = p.prefill_heads == 1 ? sg.head0
-                                              : sg.head0 + w * (p.prefill_heads / 2) + m / p.pos_block;
-        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.s.out) +
-                              ((size_t)(sg.b * p.s.Hq + head) * p.s.max_seq + t) * kHeadDim;
+        // Rows through shared memory, 64 columns at a time: a warp's 32 rows of 128 bytes (piece q of row r at q ^ (r
+        // & 7)), then eight lanes per row, so a store covers four rows of 128 bytes instead of 32 of 16.
         const float inv = l == 0.f ? 0.f : 1.f / l;
+        unsigned char* stage = tc_smem + (base - tc::smem_u32(tc_smem)) + kTcOut + (uint32_t)warp * 4096u;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.s.out);
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          uint32_t o[32];
-          tc::ld32(oa + 32 * k, o);
-          if (live) {
+        for (int half = 0; half < 2; ++half) {
+          __syncwarp();  // the other half's rows have been read
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t o[32];
+            tc::ld32(oa + 64 * half + 32 * k, o);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               uint32_t v[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 v[e] = bf16x2(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4*>(orow + 32 * k + 8 * q) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * k + q) ^ (lane & 7)) << 4)) =
+                  make_uint4(v[0], v[1], v[2], v[3]);
             }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int r = 4 * e + (lane >> 3), q = lane & 7;  // row of the warp, piece
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((q ^ (r & 7)) << 4));
+            const int mr = (warp & 3) * 32 + r;  // row of the stream
+            const int head = sg.head0 + (p.prefill_heads == 1 ? 0 : w * (p.prefill_heads >> 1) + (mr >> p.pos_shift));
+            const int tr = t_lo + (mr & (p.q_box - 1));
+            if (tr < sg.L)
+              *reinterpret_cast<uint4*>(out + ((size_t)(sg.b * p.s.Hq + head) * p.s.max_seq + tr) * kHeadDim + 64 * half +
+                                        8 * q) = v;
           }
         }
       }
@@ -769,7 +863,9 @@ cudaError_t launch_window_prefill(const hata_dims_t& d, const void* q, const voi
   p.prefill_heads = p.s.G & -p.s.G;  // a power of two, at most 16 (G <= 16)
   p.pos_block = 2 * kTcTile / p.prefill_heads;
   p.q_box = std::min(p.pos_block, kTcTile);
+  while ((1 << p.pos_shift) < p.q_box) ++p.pos_shift;
   p.n_blocks_pos = (d.max_seq + p.pos_block - 1) / p.pos_block;
+  p.rows_of_items = d.batch * (d.n_q_heads / p.prefill_heads);
   p.box_rows = kTcTile;
   const long long q_rows = (long long)d.batch * d.n_q_heads * d.max_seq, kv_rows = (long long)d.batch * d.n_kv_heads * d.max_seq;
   if (q_rows + 2 * kTcTile > 0x7fffffffLL) return cudaErrorNotSupported;
@@ -779,7 +875,8 @@ cudaError_t launch_window_prefill(const hata_dims_t& d, const void* q, const voi
     return cudaErrorNotSupported;
   cudaError_t e = configure_tc<false, false>();
   if (e != cudaSuccess) return e;
-  const long long items = (long long)p.n_blocks_pos * d.batch * (d.n_q_heads / p.prefill_heads);
+  const long long items = (long long)p.n_blocks_pos * p.rows_of_items;
+  if (items > 0x3fffffffLL) return cudaErrorNotSupported;
   const unsigned grid = (unsigned)std::min<long long>(items, span_sms());
   span_tc_kernel<false, false><<<grid, kTcThreads, kTcSmem, st>>>(qm, km, vm, p);
   return cudaGetLastError();
