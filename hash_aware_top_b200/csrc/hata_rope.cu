@@ -22,7 +22,7 @@ namespace hata {
 namespace {
 
 constexpr int kRopeWarps = 8;
-constexpr int kRopeBatch = 4;  // row steps whose loads are in flight together
+constexpr int kRopeBatch = 2;  // row steps whose loads go out together, while those of the batch before are turned
 constexpr int kRopeCtas = 3;   // per SM: 80 registers a thread
 
 struct RopeParams {
@@ -116,96 +116,86 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) norm_rope_kernel(c
     row0 = (size_t)b * p.Hkv * p.max_seq + slot;
   }
   const int half = p.rot / 2, e0 = li * N;
-  // this lane's cosines and sines (half-split: one pair per element; interleaved: one per two)
-  float c[N], sn[N];
-  int partner = lane;
+  // this lane's cosines and sines; the partner of a half-split pair is `partner`, half a rotation away
   const bool turns = e0 < p.rot;
-  float side = 0.f;  // half-split: -1 for the first element of a pair, +1 for the second
-  if (turns) {
-    const float* row = p.table + (size_t)pos * p.rot;
-    const int f0 = INTER ? e0 / 2 : (e0 < half ? e0 : e0 - half);
-    constexpr int NF = INTER ? N / 2 : N;
-#pragma unroll
-    for (int k = 0; k < NF; ++k) {
-      c[k] = __ldg(row + f0 + k);
-      sn[k] = __ldg(row + half + f0 + k);
-    }
-    if (!INTER) {
-      partner = e0 < half ? lane + half / N : lane - half / N;
-      side = e0 < half ? -1.f : 1.f;
-    }
-  }
-  float wq[N], wk[N];
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    wq[k] = p.q_weight ? __ldg(p.q_weight + e0 + k) : 1.f;
-    wk[k] = p.k_weight ? __ldg(p.k_weight + e0 + k) : 1.f;
-  }
-  const int rows = p.Hq + 2 * p.Hkv;  // query heads, key heads, value heads
-  const T* q = static_cast<const T*>(p.q_in) + tok * (size_t)p.q_stride + e0;
-  const T* kk = static_cast<const T*>(p.k_in) + tok * (size_t)p.k_stride + e0;
-  const T* v = static_cast<const T*>(p.v_in) + tok * (size_t)p.v_stride + e0;
+  const int partner = !turns || INTER ? lane : e0 < half ? lane + half / N : lane - half / N;
+  const float* trow = p.table + (size_t)pos * p.rot;
+  const int f0 = INTER ? e0 / 2 : (e0 < half ? e0 : e0 - half);
+
   const int first = sp * p.steps_per_warp * RPS;
-  const int last = min(rows, first + p.steps_per_warp * RPS);
-  auto load = [&](int r0, uint4 (&v4)[kRopeBatch]) {
+  const int last = min(p.Hq + 2 * p.Hkv, first + p.steps_per_warp * RPS);
+  // rows [lo, hi) of one kind: heads of x, normed with w (or not) and turned, to head h of dst at row stride
+  // `dst_stride`.  With y = x r w, r the reciprocal root, a turned element is r (x (w c) + x' (w' s)), x' and w' its
+  // partner's: two factors per element, made once per token.
+  auto rows_of = [&](const void* x_in, size_t x_off, const float* w, int lo, int hi, void* dst, size_t dst_row,
+                     size_t dst_stride, bool write) {
+    if (lo >= hi) return;
+    const T* x0 = static_cast<const T*>(x_in) + x_off + e0;
+    T* d0 = static_cast<T*>(dst) + dst_row * kHeadDim + e0;
+    float fa[N], fb[N];
 #pragma unroll
-    for (int u = 0; u < kRopeBatch; ++u) {
-      const int r = r0 + u * RPS + sub;
-      const T* src = r < p.Hq ? q + (size_t)r * kHeadDim
-                              : r < p.Hq + p.Hkv ? kk + (size_t)(r - p.Hq) * kHeadDim
-                                                 : v + (size_t)(r - p.Hq - p.Hkv) * kHeadDim;
-      v4[u] = r < last ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int k = 0; k < N; ++k) {
+      const float wk = w ? __ldg(w + e0 + k) : 1.f;
+      fa[k] = wk;
+      fb[k] = 0.f;
+      if (turns) {
+        const int f = INTER ? f0 + k / 2 : f0 + k;
+        const float c = __ldg(trow + f), sn = __ldg(trow + half + f);
+        const bool lead = INTER ? k % 2 == 0 : e0 < half;  // the first of its pair
+        const int pe = INTER ? e0 + (k ^ 1) : (lead ? e0 + k + half : e0 + k - half);
+        fa[k] = wk * c;
+        fb[k] = (w ? __ldg(w + pe) : 1.f) * (lead ? -sn : sn);
+      }
     }
-  };
-  uint4 in[kRopeBatch], nx[kRopeBatch];
-  load(first, nx);
-  for (int r0 = first; r0 < last; r0 += kRopeBatch * RPS) {
+    auto load = [&](int r0, uint4 (&v)[kRopeBatch]) {
 #pragma unroll
-    for (int u = 0; u < kRopeBatch; ++u) in[u] = nx[u];
-    load(r0 + kRopeBatch * RPS, nx);  // the next rows are under way while these are turned
+      for (int u = 0; u < kRopeBatch; ++u) {
+        const int r = r0 + u * RPS + sub;
+        v[u] = r < hi ? __ldg(reinterpret_cast<const uint4*>(x0 + (size_t)r * kHeadDim)) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    uint4 in[kRopeBatch], nx[kRopeBatch];
+    load(lo, nx);
+    for (int r0 = lo; r0 < hi; r0 += kRopeBatch * RPS) {
 #pragma unroll
-    for (int u = 0; u < kRopeBatch; ++u) {
-      const int r = r0 + u * RPS + sub;
-      const bool is_q = r < p.Hq, is_v = r >= p.Hq + p.Hkv;
-      float x[N];
-      Vec16<T>::unpack(in[u], x);
-      float ss = 0.f;
+      for (int u = 0; u < kRopeBatch; ++u) in[u] = nx[u];
+      load(r0 + kRopeBatch * RPS, nx);  // the next rows are under way while these are turned
 #pragma unroll
-      for (int k = 0; k < N; ++k) ss = fmaf(x[k], x[k], ss);
+      for (int u = 0; u < kRopeBatch; ++u) {
+        float x[N];
+        Vec16<T>::unpack(in[u], x);
+        float rs = 1.f;
+        if (w) {
+          float ss = 0.f;
 #pragma unroll
-      for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const bool normed = is_q ? p.q_weight != nullptr : p.k_weight != nullptr;
-      const float rs = normed ? rsqrtf(ss * (1.f / kHeadDim) + p.eps) : 1.f;
+          for (int k = 0; k < N; ++k) ss = fmaf(x[k], x[k], ss);
 #pragma unroll
-      for (int k = 0; k < N; ++k) x[k] = x[k] * rs * (is_q ? wq[k] : wk[k]);
-      if (INTER) {
-        if (turns) {
-#pragma unroll
-          for (int k = 0; k < N / 2; ++k) {
-            const float a = x[2 * k], d = x[2 * k + 1];
-            x[2 * k] = a * c[k] - d * sn[k];
-            x[2 * k + 1] = d * c[k] + a * sn[k];
-          }
+          for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          rs = rsqrtf(ss * (1.f / kHeadDim) + p.eps);
         }
-      } else if (p.rot > 0) {
+        float y[N];
 #pragma unroll
         for (int k = 0; k < N; ++k) {
-          const float other = __shfl_sync(0xffffffffu, x[k], partner);
-          if (turns) x[k] = x[k] * c[k] + side * (other * sn[k]);
+          const float other = INTER ? x[k ^ 1] : __shfl_sync(0xffffffffu, x[k], partner);
+          y[k] = rs * fmaf(x[k], fa[k], other * fb[k]);
         }
-      }
-      if (r >= last) continue;
-      const uint4 o = is_v ? in[u] : Vec16<T>::pack(x);
-      if (is_q) {
-        T* dst = static_cast<T*>(p.q_out) + (((size_t)b * p.Hq + r) * p.n_tok + i) * kHeadDim + e0;
-        *reinterpret_cast<uint4*>(dst) = o;
-      } else if (stored) {
-        const int g = is_v ? r - p.Hq - p.Hkv : r - p.Hq;
-        T* dst = static_cast<T*>(is_v ? p.V : p.K) + (row0 + (size_t)g * head_rows) * kHeadDim + e0;
-        *reinterpret_cast<uint4*>(dst) = o;
+        const int r = r0 + u * RPS + sub;
+        if (r < hi && write) *reinterpret_cast<uint4*>(d0 + (size_t)r * dst_stride * kHeadDim) = Vec16<T>::pack(y);
       }
     }
-  }
+  };
+  rows_of(p.q_in, tok * (size_t)p.q_stride, p.q_weight, first, min(last, p.Hq), p.q_out,
+          (size_t)b * p.Hq * p.n_tok + i, p.n_tok, true);
+  rows_of(p.k_in, tok * (size_t)p.k_stride, p.k_weight, max(first - p.Hq, 0), min(last - p.Hq, p.Hkv), p.K, row0,
+          head_rows, stored);
+  // values are copied
+  const T* v = static_cast<const T*>(p.v_in) + tok * (size_t)p.v_stride + e0;
+  const int v_lo = max(first - p.Hq - p.Hkv, 0), v_hi = last - p.Hq - p.Hkv;
+  if (stored)
+#pragma unroll 4
+    for (int r = v_lo + sub; r < v_hi; r += RPS)
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.V) + (row0 + (size_t)r * head_rows) * kHeadDim + e0) =
+          __ldg(reinterpret_cast<const uint4*>(v + (size_t)r * kHeadDim));
 }
 
 template <typename T, bool INTER>
