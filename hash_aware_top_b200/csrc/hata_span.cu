@@ -253,10 +253,29 @@ __global__ void __maxnreg__(kSpRegs) span_simt_kernel(const Params p) {
     const int b = pc.b, g = pc.in_seq % p.Hkv, rt = pc.in_seq / p.Hkv, j0 = pc.j0, j1 = pc.j1;
     const Seq& sq = pc.seq;
     const int r0 = rt * ROWS;
-    // queries of this unit's rows (zeros past the last)
+    auto first_slot = [&](int j) {
+      return (j < sq.sink_tiles ? j : sq.win_tile + j - sq.sink_tiles) * kSpanTile + warp * kSpKeys;
+    };
+    // the warp's rows of tile j to shared memory (zeros where nobody sees the slot)
+    auto load = [&](int j) {
+      const int s0 = first_slot(j);
+      const unsigned vis = seen_by_any16(p, sq, b, s0, lane);
+      if (!vis) return;
+      const size_t row = rows_of16<PAGED>(p, b, g, s0);
+      const unsigned char* Kg = static_cast<const unsigned char*>(p.K) + row * kHeadDim * 4 + lane * 16;
+      const unsigned char* Vg = static_cast<const unsigned char*>(p.V) + row * kHeadDim * 4 + lane * 16;
+      const uint32_t ks = ptx::smem_u32(kt) + lane * 16, vs = ptx::smem_u32(vt) + lane * 16;
+#pragma unroll
+      for (int k = 0; k < kSpKeys; ++k) {  // a row is 32 pieces of 16 bytes
+        const bool ok = (vis >> k) & 1u;
+        cp_async16_zfill(ks + k * S::kRowB, Kg + (ok ? k * kHeadDim * 4 : 0), ok);
+        cp_async16_zfill(vs + k * S::kRowB, Vg + (ok ? k * kHeadDim * 4 : 0), ok);
+      }
+    };
+    load(j0);
+    // queries of this unit's rows (zeros past the last), while the first rows are under way
     const T* q = static_cast<const T*>(p.q) + (((size_t)b * p.Hq + (size_t)g * p.G) * p.T + r0) * kHeadDim;
-    for (int e = tid; e < ROWS * kHeadDim; e += kSpThreads)
-      sm_q[e] = r0 + e / kHeadDim < p.R ? q[e] : 0.f;
+    for (int e = tid; e < ROWS * kHeadDim; e += kSpThreads) sm_q[e] = r0 + e / kHeadDim < p.R ? q[e] : 0.f;
     __syncthreads();
     float m[ROWS], l[ROWS], o[ROWS][4];
 #pragma unroll
@@ -267,22 +286,17 @@ __global__ void __maxnreg__(kSpRegs) span_simt_kernel(const Params p) {
       for (int k = 0; k < 4; ++k) o[r][k] = 0.f;
     }
     for (int j = j0; j < j1; ++j) {
-      const int tile = j < sq.sink_tiles ? j : sq.win_tile + j - sq.sink_tiles;
-      const int s0 = tile * kSpanTile + warp * kSpKeys;
-      const unsigned vis = seen_by_any16(p, sq, b, s0, lane);
-      if (!vis) continue;  // the warp's slots are seen by nobody
-      const size_t row = rows_of16<PAGED>(p, b, g, s0);
-      constexpr int VPR = kHeadDim * (int)sizeof(T) / 16;  // vectors of a row
-      const unsigned char* Kg = static_cast<const unsigned char*>(p.K) + row * kHeadDim * sizeof(T);
-      const unsigned char* Vg = static_cast<const unsigned char*>(p.V) + row * kHeadDim * sizeof(T);
-      __syncwarp();  // the last tile's rows and probabilities have been read
-      for (int e = lane; e < kSpKeys * VPR; e += 32) {
-        const int k = e / VPR, c = e % VPR;
-        const bool ok = (vis >> k) & 1u;
-        const size_t off = ok ? (size_t)k * kHeadDim * sizeof(T) + c * 16 : 0;
-        cp_async16_zfill(ptx::smem_u32(kt) + k * S::kRowB + c * 16, Kg + off, ok);
-        cp_async16_zfill(ptx::smem_u32(vt) + k * S::kRowB + c * 16, Vg + off, ok);
+      if (j > j0) {
+        __syncwarp();  // the last tile's rows and probabilities have been read
+        load(j);
       }
+      const int s0 = first_slot(j);
+      const unsigned vis = seen_by_any16(p, sq, b, s0, lane);
+      if (!vis) continue;  // nobody sees the warp's slots
+      const bool all_see = vis == 0xffffu && s0 + kSpKeys <= sq.ctx;
+      // lane r: what row r sees of the 16 slots
+      uint32_t bits = vis;
+      if (s0 + kSpKeys > sq.ctx && lane < ROWS) bits &= row_bits(p, sq, b, (r0 + lane) % p.T, s0);
       ptx::cp_async_wait_all();
       __syncwarp();
       // logits of this lane's slot: dimensions 8 c + 4 half .. + 3
@@ -299,13 +313,11 @@ __global__ void __maxnreg__(kSpRegs) span_simt_kernel(const Params p) {
           acc[r] = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, fmaf(qv.z, kv.z, fmaf(qv.w, kv.w, acc[r]))));
         }
       }
-      const int s = s0 + key;
-      const bool live = (vis >> key) & 1u;
-      const bool all_see = s0 + kSpKeys <= sq.ctx;
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
         float x = (acc[r] + __shfl_xor_sync(0xffffffffu, acc[r], 16)) * p.scale_log2;
-        if (!live || (!all_see && !sees(p, sq, b, (r0 + r) % p.T, s))) x = -INFINITY;
+        const uint32_t row = __shfl_sync(0xffffffffu, bits, r);
+        if (!all_see && !((row >> key) & 1u)) x = -INFINITY;
         float mx = x;
 #pragma unroll
         for (int w = 8; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
@@ -492,10 +504,20 @@ __global__ void __maxnreg__(kSpRegs) span_mma_kernel(const Params p) {
     for (int j = j0; j < j1; ++j) {
       __syncwarp();  // every lane is done with the stage that this load fills
       load(j + kMmStages - 1);
-      asm volatile("cp.async.wait_group %0;\n" ::"n"(kMmStages - 1) : "memory");
-      __syncwarp();
       const int s0 = first_slot(j);
       const unsigned vis = seen_by_any16(p, sq, b, s0, lane);
+      const bool all_see = vis == 0xffffu && s0 + kSpKeys <= sq.ctx;
+      uint32_t bits[MT][2];  // what this lane's rows see of the 16 slots
+      if (!all_see && vis)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            bits[mt][h] = vis;
+            if (s0 + kSpKeys > sq.ctx) bits[mt][h] &= row_bits(p, sq, b, (r0 + 16 * mt + gq + 8 * h) % p.T, s0);
+          }
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(kMmStages - 1) : "memory");
+      __syncwarp();
       if (!vis) continue;  // nobody sees the warp's slots
       const uint32_t st = stages_u + (uint32_t)((j % kMmStages) * kMmStageB), kt = st + kfrag, vt = st + vfrag;
       float s[MT][2][4];
@@ -516,7 +538,6 @@ __global__ void __maxnreg__(kSpRegs) span_mma_kernel(const Params p) {
           mma16816(s[mt][1], qa[MT > 1 ? 0 : ks], kb[2], kb[3]);
         }
       }
-      const bool all_see = vis == 0xffffu && s0 + kSpKeys <= sq.ctx;
       bool moves = false;
       float x_max[MT][2];
 #pragma unroll
@@ -529,11 +550,7 @@ __global__ void __maxnreg__(kSpRegs) span_mma_kernel(const Params p) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               float x = s[mt][n][2 * h + k];
-              if (!all_see) {
-                const int e = 8 * n + 2 * cq + k;
-                if (!((vis >> e) & 1u) || (s0 + e >= sq.ctx && !sees(p, sq, b, (r0 + 16 * mt + gq + 8 * h) % p.T, s0 + e)))
-                  x = -INFINITY;
-              }
+              if (!all_see && !((bits[mt][h] >> (8 * n + 2 * cq + k)) & 1u)) x = -INFINITY;
               s[mt][n][2 * h + k] = x;
               mx = fmaxf(mx, x);
             }

@@ -266,16 +266,19 @@ __device__ __forceinline__ Runs runs_of(const Params& p, int lane, int grid, int
   return r;
 }
 
-// Whether new token i sees slot s, a slot that some token may see.
-__device__ __forceinline__ bool sees(const Params& p, const Seq& q, int b, int i, int s) {
-  const int j = s - q.ctx;
-  if (j < 0) return true;
-  if (!p.mask) return j <= i;
-  return (p.mask[((size_t)b * p.T + i) * p.mask_words + (j >> 5)] >> (j & 31)) & 1u;
-}
-
 // The n lowest bits (none below 1, all from 32 on).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// Bit k: new token i sees slot s0 + k (k < 32), of those that some token may see.
+__device__ __forceinline__ uint32_t row_bits(const Params& p, const Seq& q, int b, int i, int s0) {
+  const int j0 = s0 - q.ctx;  // the new token that slot s0 holds; before 0: context, seen by all
+  if (!p.mask) return low_bits(i + 1 - j0);
+  const uint32_t* row = p.mask + ((size_t)b * p.T + i) * p.mask_words;
+  const int w = j0 >> 5;
+  const uint32_t lo = w < 0 ? 0xffffffffu : w < p.mask_words ? __ldg(row + w) : 0u;
+  const uint32_t hi = w + 1 < 0 ? 0xffffffffu : w + 1 < p.mask_words ? __ldg(row + w + 1) : 0u;
+  return __funnelshift_r(lo, hi, j0 & 31);
+}
 
 // A slot that no token sees may hold anything (a value row that is not finite would turn 0 * V into NaN), so
 // it is read as zeros.  Bit k of the answer: some token sees slot s0 + k (k < 16).  All lanes of a warp.
@@ -285,11 +288,8 @@ __device__ __forceinline__ unsigned seen_by_any16(const Params& p, const Seq& q,
   if (p.window > 0) in &= low_bits(p.sink - s0) | ~low_bits(q.L - min(p.window, q.L) - s0);
   if (s0 + 16 <= q.ctx || !p.mask || !in) return in;
   unsigned any = 0;
-  for (int i = lane; i < q.n_b; i += 32)
-    for (int k = max(0, q.ctx - s0); k < 16; ++k)
-      if ((in >> k) & 1u) any |= sees(p, q, b, i, s0 + k) ? 1u << k : 0u;
-  any = __reduce_or_sync(0xffffffffu, any);
-  return in & (any | low_bits(q.ctx - s0));  // slots before the new tokens are seen by all
+  for (int i = lane; i < q.n_b; i += 32) any |= row_bits(p, q, b, i, s0);
+  return in & __reduce_or_sync(0xffffffffu, any);
 }
 
 }  // namespace span
