@@ -296,6 +296,7 @@ __global__ void __maxnreg__(kTcRegs)
   const uint32_t tmem = tmem_s;
 
   auto wait_ok = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (tc::mbar_wait(bar, parity, 1)) return true;
     for (uint32_t it = 0; it < kTcTries; it += 64) {
       if (abort_s) return false;
       if (tc::mbar_wait(bar, parity, 64)) return true;
@@ -410,30 +411,24 @@ __global__ void __maxnreg__(kTcRegs)
     for (int n_seg = 0; ok && walk.next(sg); ++n_seg) {
       const int n = __shfl_sync(0xffffffffu, sg.j1 - sg.j0, 0), steps = steps_of(n);
       ok = wait_warp(&q_full, (uint32_t)(n_seg & 1));
+      auto slot_of = [&](int k) { return (item0 + (uint32_t)k) % kStages; };
       auto wait_item = [&](int k) {
         const uint32_t it = item0 + (uint32_t)k;
         return wait_warp(&full[it % kStages], (it / kStages) & 1);
       };
-      auto stage_of = [&](int k) { return base + kTcRing + ((item0 + (uint32_t)k) % kStages) * kTcTileB; };
-      auto free_item = [&](int k) { commit_elected(&freed[(item0 + (uint32_t)k) % kStages]); };
-      auto issue_s = [&](int i, int w) {
-        tc::fence_after();
-        mma8_s(tmem + (uint32_t)w * kTcTile, tc::desc_kmajor_sw128(base + kTcQ + (pair ? (uint32_t)w * kTcTileB : 0u)),
-               tc::desc_kmajor_sw128(stage_of(item_k(i, w))), idS);
-        commit_elected(&s_full[w]);
-      };
-      auto issue_pv = [&](int i, int w, int half) {
-        tc::fence_after();
-        mma4_pv(tmem + 256u + (uint32_t)w * kHeadDim, tmem + (uint32_t)(w * kTcTile + half * 32),
-                tc::desc_mnmajor_sw128(stage_of(item_v(n, i, w)) + (uint32_t)half * 8192u, (uint32_t)(kTcTileB / 2)),
-                idPV, (i > 0 || half) ? 1u : 0u);
-      };
+      const uint64_t q_desc[2] = {tc::desc_kmajor_sw128(base + kTcQ),
+                                  tc::desc_kmajor_sw128(base + kTcQ + (pair ? (uint32_t)kTcTileB : 0u))};
+      auto k_desc = [&](uint32_t slot) { return tc::desc_kmajor_sw128(base + kTcRing + slot * kTcTileB); };
       const int s0n = pair ? 2 : streams_in(n, 0);  // streams of the first step
-#pragma unroll 1
-      for (int w = 0; ok && w < s0n; ++w) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (!ok || w >= s0n) break;
         if ((!pair || w == 0) && !(ok = wait_item(item_k(0, w)))) break;
-        issue_s(0, w);
-        if (!pair || w == 1) free_item(item_k(0, w));
+        const uint32_t ks = slot_of(item_k(0, w));
+        tc::fence_after();
+        mma8_s(tmem + (uint32_t)w * kTcTile, q_desc[w], k_desc(ks), idS);
+        commit_elected(&s_full[w]);
+        if (!pair || w == 1) commit_elected(&freed[ks]);
       }
       if (ok && steps == 1) commit_elected(&q_free);
 #pragma unroll 1
@@ -443,22 +438,30 @@ __global__ void __maxnreg__(kTcRegs)
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (!ok || w >= m) break;
-          uint32_t& done = w ? done1 : done0;
+          // the tiles first: when P comes, its PV and the next S go out at once
           if ((!pair || w == 0) && !(ok = wait_item(item_v(n, i, w)))) break;
+          if ((!pair || w == 0) && w < m_next && !(ok = wait_item(item_k(i + 1, w)))) break;
+          const uint32_t vs = slot_of(item_v(n, i, w)), ks = slot_of(item_k(i + 1, w));
+          const uint64_t vd = tc::desc_mnmajor_sw128(base + kTcRing + vs * kTcTileB, (uint32_t)(kTcTileB / 2));
+          const uint64_t kd = k_desc(ks);
+          uint32_t& done = w ? done1 : done0;
+          const uint32_t o = tmem + 256u + (uint32_t)w * kHeadDim, sp = tmem + (uint32_t)(w * kTcTile);
           if (!(ok = wait_warp(&p_half[w], done & 1))) break;
-          issue_pv(i, w, 0);
+          tc::fence_after();
+          mma4_pv(o, sp, vd, idPV, i > 0 ? 1u : 0u);
           if (!(ok = wait_warp(&p_full[w], done & 1))) break;
           ++done;
-          issue_pv(i, w, 1);
-          if (!pair || w == 1) free_item(item_v(n, i, w));
+          tc::fence_after();
+          mma4_pv(o, sp + 32u, vd + 512u, idPV, 1u);
           if (w < m_next) {
-            if ((!pair || w == 0) && !(ok = wait_item(item_k(i + 1, w)))) break;
-            issue_s(i + 1, w);
-            if (!pair || w == 1) free_item(item_k(i + 1, w));
+            mma8_s(sp, q_desc[w], kd, idS);
+            commit_elected(&s_full[w]);
+            if (!pair || w == 1) commit_elected(&freed[ks]);
             if (i + 2 == steps && w == m_next - 1) commit_elected(&q_free);
           } else {
             commit_elected(&o_full[w]);  // the stream's last PV
           }
+          if (!pair || w == 1) commit_elected(&freed[vs]);
         }
       }
       item0 += (uint32_t)(2 * n);
