@@ -296,7 +296,8 @@ __device__ __forceinline__ unsigned seen_by_any16(const Params& p, const Seq& q,
 
 // Whether the counts of the split fit their types.
 inline bool span_fits(const span::Params& p, long long units) {
-  return units * ((p.max_seq + span::kSpanTile - 1LL) / span::kSpanTile) <= 0x3fffffffLL && span_sms() <= 255;
+  return p.max_seq <= 0x7fffff00 && span_sms() <= 255 &&
+         units * ((p.max_seq + span::kSpanTile - 1LL) / span::kSpanTile) <= 0x3fffffffLL;
 }
 
 // Launches a kernel that may be set up while the one before it on the stream runs (and waits for it with
@@ -312,7 +313,9 @@ cudaError_t launch_early(void (*k)(Args...), dim3 grid, unsigned threads, cudaSt
   cfg.stream = st;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, args...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e;
 }
 
 // Tensor-core form of tree attention (hata_span_tc.cu): bf16, any number of rows.

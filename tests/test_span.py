@@ -185,6 +185,24 @@ def test_tree_heads(H, dtype, Hq, Hkv):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bs", [0, 16])
+@pytest.mark.parametrize("T,max_seq", [(3, 5), (9, 9), (20, 130)])
+def test_tree_caches_smaller_than_a_tile(H, bs, T, max_seq):
+    tree_case(H, torch.bfloat16, 1, T, 16, 1, max_seq, bs, [max_seq], [T], seed=T)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,Hq", [(7, 4), (40, 4)])
+def test_tree_many_sequences(H, dtype, T, Hq):
+    """More sequences than a warp scans at a time, some without new tokens."""
+    B = 45
+    lens = [T + (61 * b) % 300 for b in range(B)]
+    n_new = [0 if b % 7 == 3 else T - b % 3 for b in range(B)]
+    tree_case(H, dtype, B, T, Hq, 1, 400, 16, lens, n_new, seed=B)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("T,Hq,Hkv", [(5, 4, 4), (40, 4, 1), (128, 8, 2)])
 def test_tree_masks_that_leave_rows_empty(H, dtype, T, Hq, Hkv):
