@@ -1,7 +1,7 @@
 // Window decode and tree attention: softmax(scale * q . K) V of the new tokens' rows over the visible slots
 // of a contiguous or paged cache (hata_span.cuh has the split of the work).
 //
-// span_mma_kernel (bf16, up to 32 rows per KV head): eight warps, each with 16 slots of a 128-slot tile, on its own: it
+// span_mma_kernel (bf16, tiles of up to 32 rows per KV head): eight warps, each with 16 slots of a 128-slot tile, on its own: it
 // streams its rows of K and V through three shared-memory stages (cp.async, 16-byte pieces swizzled so that the eight
 // rows of a fragment lie in distinct banks), computes S on m16n8k16 tiles with the query rows as M, turns S
 // into P in place (the accumulator of S has the layout of the A operand of P.V), and adds P.V to its own running
@@ -675,10 +675,15 @@ cudaError_t launch_mma(const Params& p, bool paged, cudaStream_t st) {
 // rows of the largest row tile of the kernels here
 constexpr int kSpanMaxRows = 32;
 
-// bf16 with more rows per KV head than this runs on the tensor cores.
-constexpr int kSpanTcRows = 32;
+// bf16 with more rows per KV head than a tile of span_mma_kernel holds runs on span_tc_kernel.  Up to two such tiles, both
+// of which read all keys, are faster while the keys are few and the fixed costs count: 64 rows, 8 KV heads (tiles of 128
+// slots in all: us of span_mma_kernel, of span_tc_kernel): 256: 15, 20; 2048: 45, 50; 8192: 181, 111.
+constexpr int kSpanTcRows = 32, kSpanTcTiles = 2048;
 bool use_tc(const hata_dims_t& d, int n_tok) {
-  return d.dtype == HATA_BF16 && (d.n_q_heads / d.n_kv_heads) * n_tok > kSpanTcRows;
+  const long long rows = (long long)(d.n_q_heads / d.n_kv_heads) * n_tok;
+  if (d.dtype != HATA_BF16 || rows <= kSpanTcRows) return false;
+  const long long tiles = (long long)d.batch * d.n_kv_heads * ((d.max_seq + kSpanTile - 1LL) / kSpanTile);
+  return rows > 2 * kSpanTcRows || tiles > kSpanTcTiles;
 }
 
 }  // namespace

@@ -748,43 +748,62 @@ __global__ void __maxnreg__(kTcRegs)
   }
 }
 
-// Joins the partials of a unit: thread (row, 4 columns), partials in the order of the split.
+// Joins the partials of a unit in the order of the split: thread (row, 4 columns).  The partials were just written by
+// other SMs: six of them are under way at a time (one after another, 36 partials of a unit took 25 us).
 // grid = (units, 32, row tiles of a unit).
-constexpr int kMergeCols = 1;  // column quads of a CTA
-__global__ void __launch_bounds__(kTcTile* kMergeCols) span_merge_kernel(const TcParams p, int grid_tc, int rows_per_unit) {
+constexpr int kMergeBatch = 6;
+constexpr int kMergeRegs = 56;  // 128 threads of these fit beside the main kernel's CTA
+__global__ void __maxnreg__(kMergeRegs) span_merge_kernel(const TcParams p, int grid_tc, int rows_per_unit) {
   const int lane = threadIdx.x & 31;
   const int upt = p.s.Hkv * p.s.row_tiles, unit = (int)blockIdx.x, b = unit / upt, in_seq = unit % upt;
   // the lengths are the call's inputs: where the partials lie is found while the main kernel still runs
   const span::Seq sq = span::seq_of(p.s, b);
   if (sq.tiles == 0) return;
   const span::Runs runs = span::runs_of(p.s, lane, grid_tc, b, in_seq, sq);
-  ptx::pdl_wait();
-  const int c0 = runs.cta0, c1 = runs.cta0 + runs.n - 1;
-  const int g = in_seq % p.s.Hkv, r0 = in_seq / p.s.Hkv * rows_per_unit;
-  const int half = blockIdx.z;  // pair: which of the two row tiles
-  const int m = threadIdx.x % kTcTile, q4 = (int)blockIdx.y * kMergeCols + threadIdx.x / kTcTile;
-  const int row = r0 + half * kTcTile + m;
+  const int g = in_seq % p.s.Hkv, half = blockIdx.z;  // half: of a pair, the row tile
+  const int m = threadIdx.x, q4 = (int)blockIdx.y;
+  const int row = in_seq / p.s.Hkv * rows_per_unit + half * kTcTile + m;
   if (row >= p.s.R || row % p.s.T >= sq.n_b) return;
-  const int n_str = p.pair ? 1 : 2;  // partials of a row in one run
-  auto part = [&](int c, int w) { return p.s.part + ((size_t)(unit + c) * 2 + (p.pair ? half : w)) * kPartFloats; };
-  float M = -INFINITY;
-  for (int c = c0; c <= c1; ++c)
-    for (int w = 0; w < n_str; ++w) M = fmaxf(M, __ldcg(part(c, w) + m));
-  float l = 0.f;
+  // a row's partials: one per run and, if its key tiles were shared out over both streams, stream
+  const int n_str = p.pair ? 1 : 2, n = runs.n * n_str;
+  const float* first = p.s.part + ((size_t)(unit + runs.cta0) * 2 + (p.pair ? half : 0)) * kPartFloats + m;
+  const size_t step = (size_t)kPartFloats * (p.pair ? 2 : 1);
+  ptx::pdl_wait();
+  float M = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = c0; c <= c1; ++c)
-    for (int w = 0; w < n_str; ++w) {
-      const float* pp = part(c, w);
-      const float mc = __ldcg(pp + m);
-      if (mc == -INFINITY) continue;  // nothing seen in this run (or the stream had no tile: O was not written)
-      const float f = exp2f(mc - M);
-      l = fmaf(__ldcg(pp + kTcTile + m), f, l);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(pp + 2 * kTcTile) + (size_t)q4 * kTcTile + m);
-      o.x = fmaf(v.x, f, o.x);
-      o.y = fmaf(v.y, f, o.y);
-      o.z = fmaf(v.z, f, o.z);
-      o.w = fmaf(v.w, f, o.w);
+  for (int i0 = 0; i0 < n; i0 += kMergeBatch) {
+    float mi[kMergeBatch], li[kMergeBatch];
+    float4 v[kMergeBatch];
+#pragma unroll
+    for (int k = 0; k < kMergeBatch; ++k) {
+      const float* pp = first + (size_t)(i0 + k) * step;
+      const bool in = i0 + k < n;
+      mi[k] = in ? __ldcg(pp) : -INFINITY;
+      li[k] = in ? __ldcg(pp + kTcTile) : 0.f;
+      v[k] = in ? __ldcg(reinterpret_cast<const float4*>(pp + 2 * kTcTile - m) + (size_t)q4 * kTcTile + m)
+                : make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    float m_new = M;
+#pragma unroll
+    for (int k = 0; k < kMergeBatch; ++k) m_new = fmaxf(m_new, mi[k]);
+    const float back = m_new == -INFINITY ? 1.f : exp2f(M - m_new);
+    M = m_new;
+    l *= back;
+    o.x *= back;
+    o.y *= back;
+    o.z *= back;
+    o.w *= back;
+#pragma unroll
+    for (int k = 0; k < kMergeBatch; ++k) {
+      if (mi[k] == -INFINITY) continue;  // nothing seen in this run (or the stream had no tile: O was not written)
+      const float f = exp2f(mi[k] - M);
+      l = fmaf(li[k], f, l);
+      o.x = fmaf(v[k].x, f, o.x);
+      o.y = fmaf(v[k].y, f, o.y);
+      o.z = fmaf(v[k].z, f, o.z);
+      o.w = fmaf(v[k].w, f, o.w);
+    }
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.s.out) +
                        (((size_t)b * p.s.Hq + (size_t)g * p.s.G) * p.s.T + row) * kHeadDim + 4 * q4;
@@ -840,8 +859,7 @@ cudaError_t launch_span_tc(const hata_dims_t& d, const span::Params& s, const Pa
   if (pg) span_tc_kernel<true, true><<<sms, kTcThreads, kTcSmem, st>>>(qm, km, vm, p);
   else span_tc_kernel<true, false><<<sms, kTcThreads, kTcSmem, st>>>(qm, km, vm, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_early(span_merge_kernel, dim3((unsigned)units, kHeadDim / 4 / kMergeCols, p.pair ? 2 : 1),
-                      kTcTile * kMergeCols, st, p, sms, rows);
+  return launch_early(span_merge_kernel, dim3((unsigned)units, kHeadDim / 4, p.pair ? 2 : 1), kTcTile, st, p, sms, rows);
 }
 
 cudaError_t launch_window_prefill(const hata_dims_t& d, const void* q, const void* K, const void* V,

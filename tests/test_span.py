@@ -172,7 +172,7 @@ def tree_case(H, dtype, B, T, Hq, Hkv, max_seq, bs, lens, n_new, mask="tree", se
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("bs", [0, 16, 256])
-@pytest.mark.parametrize("T", [1, 2, 7, 31, 33, 64, 100, 128])
+@pytest.mark.parametrize("T", [1, 2, 7, 9, 16, 31, 33, 64, 100, 128])
 def test_tree(H, dtype, bs, T):
     tree_case(H, dtype, 3, T, 8, 2, 700, bs, [700, T, T + 131], [T, T, max(1, T - 1)], seed=T)
 
@@ -193,7 +193,7 @@ def test_tree_caches_smaller_than_a_tile(H, bs, T, max_seq):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("T,Hq", [(7, 4), (40, 4)])
+@pytest.mark.parametrize("T,Hq", [(7, 4), (13, 4), (40, 4)])
 def test_tree_many_sequences(H, dtype, T, Hq):
     """More sequences than a warp scans at a time, some without new tokens."""
     B = 45
@@ -208,6 +208,13 @@ def test_tree_many_sequences(H, dtype, T, Hq):
 def test_tree_masks_that_leave_rows_empty(H, dtype, T, Hq, Hkv):
     tree_case(H, dtype, 3, T, Hq, Hkv, 400, 16, [T, T + 3, 0], [T, T, 0], mask=0.2, seed=T)
     tree_case(H, dtype, 3, T, Hq, Hkv, 400, 0, [T, 400, 130], [T, T, T if T < 130 else 130], mask=0.0, seed=T)
+
+
+@pytest.mark.gpu
+def test_tree_of_some_rows_over_a_long_cache(H):
+    """Rows that a short cache gives to one kernel and a long one to the other."""
+    tree_case(H, torch.bfloat16, 1, 12, 8, 2, 140000, 256, [139999], [12], seed=4)
+    tree_case(H, torch.bfloat16, 1, 12, 8, 2, 4000, 256, [3999], [11], seed=4)
 
 
 @pytest.mark.gpu
