@@ -7,6 +7,8 @@ would otherwise be read by a kernel), then passes data pointers and the current
 CUDA stream to the library.  All computation happens in the CUDA kernels of
 libhata.so; there is no CPU fallback, and importing this package fails loudly
 when the library has not been built (python hash_aware_top_b200/build.py).
+Most calls go through ctypes; those of the serving operators through a native
+module (_serving) with the same checks.
 
 Function names and argument order follow include/hata.h.
 """
@@ -198,6 +200,8 @@ def _load():
 
 
 lib = _load()
+
+from . import _serving  # noqa: E402  (native; needs libhata.so, which is loaded now)
 
 
 def hata_status_string(status: int) -> str:
@@ -497,77 +501,12 @@ def hata_decode_step_paged(dims: Dims, q, K_pool, V_pool, W_q, W_k, codes_pool, 
 
 
 # --- serving operators beside the decode step -----------------------------------------------------------
+# Their arguments are checked, as above, by the native half of the binding (binding/serving.cpp): in Python the checks took
+# longer than the smallest of these kernels.
 
 
-def _device() -> int:
-    """The current device; where there is none, a number that no tensor has."""
-    try:
-        return torch.cuda.current_device()
-    except (RuntimeError, AssertionError):
-        return -2
-
-
-def _dptr(t, name, shape, dtype, dev, optional=False):
-    """Address of a contiguous tensor of this shape and type on the current device `dev` (None if optional)."""
-    if t is None and optional:
-        return None
-    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype and t.shape == shape
-            and t.is_contiguous()):
-        return t.data_ptr()
-    if t is None:
-        raise ValueError(f"{name} is required")
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on the current device (got {t.device})")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _ws(ws, dev):
-    """Address and size of a uint8 workspace on the current device."""
-    n = ws.numel() if isinstance(ws, torch.Tensor) else 0
-    return _dptr(ws, "workspace", (n,), torch.uint8, dev), n
-
-
-def _token_rows(t, name, d: Dims, heads: int, n_tok: int, dev):
-    """Address and token stride of [B][n_tok][heads][d], heads contiguous, tokens at any one stride (a part of a
-    projection's output, for instance)."""
-    B, D = d.batch, d.head_dim
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on the current device (got {t.device})")
-    if t.dtype is not d.torch_dtype:
-        raise TypeError(f"{name} must be {d.torch_dtype} (got {t.dtype})")
-    if t.shape != (B, n_tok, heads, D):
-        raise ValueError(f"{name} must have shape {(B, n_tok, heads, D)} (got {tuple(t.shape)})")
-    sb, st, sh, se = t.stride()
-    if se != 1 or (heads > 1 and sh != D) or (n_tok > 1 and B > 1 and sb != n_tok * st):
-        raise ValueError(f"{name} must hold each token's heads side by side and its tokens at one stride "
-                         f"(strides {t.stride()})")
-    return t.data_ptr(), st if n_tok > 1 else sb if B > 1 else heads * D
-
-
-def _cache_args(d: Dims, dev, K, V):
-    """Addresses of a contiguous cache."""
-    shape, t = (d.batch, d.n_kv_heads, d.max_seq, d.head_dim), d.torch_dtype
-    return _dptr(K, "K", shape, t, dev), _dptr(V, "V", shape, t, dev)
-
-
-def _pool_args(d: Dims, dev, K_pool, V_pool, block_table, block_size):
-    """Addresses of paged pools and of their table."""
-    bs = int(block_size)
-    if not isinstance(K_pool, torch.Tensor) or K_pool.dim() != 4:
-        raise ValueError("K_pool must be a tensor [n_blocks][Hkv][block_size][d]")
-    n_blocks, t = K_pool.shape[0], d.torch_dtype
-    pool = (n_blocks, d.n_kv_heads, bs, d.head_dim)
-    return (_dptr(K_pool, "K_pool", pool, t, dev), _dptr(V_pool, "V_pool", pool, t, dev),
-            _dptr(block_table, "block_table", (d.batch, -(-d.max_seq // bs) if bs > 0 else 0), torch.int32, dev), bs,
-            n_blocks)
+def _handle(stream):
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
 def hata_rope_table(n_pos, rot_dim, theta, stream=None) -> torch.Tensor:
@@ -578,51 +517,24 @@ def hata_rope_table(n_pos, rot_dim, theta, stream=None) -> torch.Tensor:
     return table
 
 
-def _norm_rope_args(d, dev, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions, seq_lens, q_out):
-    if not isinstance(q_in, torch.Tensor) or q_in.dim() != 4:
-        raise ValueError("q_in must be a tensor [B][n_tok][Hq][d]")
-    T, w = q_in.shape[1], (d.head_dim,)
-    n_pos = rot = 0
-    if table is not None:
-        if not isinstance(table, torch.Tensor) or table.dim() != 3:
-            raise ValueError("table must be a tensor [n_pos][2][rot_dim / 2]")
-        n_pos, rot = table.shape[0], 2 * table.shape[2]
-        table = _dptr(table, "table", (n_pos, 2, rot // 2), torch.float32, dev)
-    return (ctypes.byref(d), T, *_token_rows(q_in, "q_in", d, d.n_q_heads, T, dev), *_token_rows(k_in, "k_in", d, d.n_kv_heads, T, dev),
-            *_token_rows(v_in, "v_in", d, d.n_kv_heads, T, dev), _dptr(q_weight, "q_weight", w, torch.float32, dev, True),
-            _dptr(k_weight, "k_weight", w, torch.float32, dev, True), float(eps), table, n_pos, rot, int(bool(interleaved)),
-            _dptr(n_new, "n_new", (d.batch,), torch.int32, dev, True),
-            _dptr(positions, "positions", (d.batch, T), torch.int32, dev, True),
-            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32, dev),
-            _dptr(q_out, "q_out", (d.batch, d.n_q_heads, T, d.head_dim), d.torch_dtype, dev))
-
-
 def hata_norm_rope(dims: Dims, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions,
                    seq_lens, q_out, K, V, ws, stream=None):
     """Norm and rotate the heads of q_in and k_in ([B][n_tok][heads][d], any token stride), writing q_out
     ([B][Hq][n_tok][d]) and the K and V cache rows of the new tokens, the last of seq_lens[b]."""
-    dev = _device()
-    _check(
-        lib.hata_norm_rope(
-            *_norm_rope_args(dims, dev, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions,
-                             seq_lens, q_out), *_cache_args(dims, dev, K, V), *_ws(ws, dev), _stream(stream)),
-        "hata_norm_rope")
+    _check(_serving.norm_rope(dims, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions, seq_lens,
+                              q_out, K, V, None, 0, ws, _handle(stream), False), "hata_norm_rope")
 
 
 def hata_norm_rope_paged(dims: Dims, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions,
                          seq_lens, q_out, K_pool, V_pool, block_table, block_size, ws, stream=None):
     """hata_norm_rope into paged pools ([n_blocks][Hkv][block_size][d])."""
-    dev = _device()
-    _check(
-        lib.hata_norm_rope_paged(
-            *_norm_rope_args(dims, dev, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions,
-                             seq_lens, q_out), *_pool_args(dims, dev, K_pool, V_pool, block_table, block_size), *_ws(ws, dev),
-            _stream(stream)),
-        "hata_norm_rope_paged")
+    _check(_serving.norm_rope(dims, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions, seq_lens,
+                              q_out, K_pool, V_pool, block_table, block_size, ws, _handle(stream), True),
+           "hata_norm_rope_paged")
 
 
 def hata_span_workspace_size(dims: Dims, n_tok: int = 1) -> int:
-    """Bytes of workspace of hata_window_decode (n_tok = 1) and hata_tree_attention; zero it once."""
+    """Bytes of workspace of hata_window_decode (n_tok = 1) and hata_tree_attention."""
     n = ctypes.c_size_t(0)
     _check(lib.hata_span_workspace_size(ctypes.byref(dims), int(n_tok), ctypes.byref(n)), "hata_span_workspace_size")
     return n.value
@@ -630,77 +542,36 @@ def hata_span_workspace_size(dims: Dims, n_tok: int = 1) -> int:
 
 def hata_window_decode(dims: Dims, q, K, V, seq_lens, window, n_sink, scale, out, ws, stream=None):
     """Decode attention over the last `window` slots and the first `n_sink` of each sequence."""
-    d = dims
-    dev = _device()
-    row = (d.batch, d.n_q_heads, d.head_dim)
-    _check(
-        lib.hata_window_decode(
-            ctypes.byref(d), _dptr(q, "q", row, d.torch_dtype, dev), *_cache_args(d, dev, K, V),
-            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32, dev), int(window), int(n_sink), float(scale),
-            _dptr(out, "out", row, d.torch_dtype, dev), *_ws(ws, dev), _stream(stream)),
-        "hata_window_decode")
+    _check(_serving.window_decode(dims, q, K, V, None, 0, seq_lens, window, n_sink, scale, out, ws, _handle(stream), False),
+           "hata_window_decode")
 
 
 def hata_window_decode_paged(dims: Dims, q, K_pool, V_pool, block_table, block_size, seq_lens, window, n_sink, scale,
                              out, ws, stream=None):
     """hata_window_decode over paged pools."""
-    d = dims
-    dev = _device()
-    row = (d.batch, d.n_q_heads, d.head_dim)
-    _check(
-        lib.hata_window_decode_paged(
-            ctypes.byref(d), _dptr(q, "q", row, d.torch_dtype, dev), *_pool_args(d, dev, K_pool, V_pool, block_table, block_size),
-            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32, dev), int(window), int(n_sink), float(scale),
-            _dptr(out, "out", row, d.torch_dtype, dev), *_ws(ws, dev), _stream(stream)),
-        "hata_window_decode_paged")
+    _check(_serving.window_decode(dims, q, K_pool, V_pool, block_table, block_size, seq_lens, window, n_sink, scale, out, ws,
+                                  _handle(stream), True), "hata_window_decode_paged")
 
 
 def hata_window_prefill(dims: Dims, q, K, V, seq_lens, window, n_sink, scale, out, ws, stream=None):
     """Causal prefill attention (q/out [B][Hq][max_seq][d], K/V [B][Hkv][max_seq][d], bf16) over the last `window`
     positions and the first `n_sink`."""
-    d = dims
-    dev = _device()
-    rows = (d.batch, d.n_q_heads, d.max_seq, d.head_dim)
-    _check(
-        lib.hata_window_prefill(
-            ctypes.byref(d), _dptr(q, "q", rows, d.torch_dtype, dev), *_cache_args(d, dev, K, V),
-            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32, dev), int(window), int(n_sink), float(scale),
-            _dptr(out, "out", rows, d.torch_dtype, dev), *_ws(ws, dev), _stream(stream)),
-        "hata_window_prefill")
-
-
-def _tree_args(d, dev, q, seq_lens, n_new, mask, out):
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
-        raise ValueError("q must be a tensor [B][Hq][n_tok][d]")
-    T = q.shape[2]
-    rows = (d.batch, d.n_q_heads, T, d.head_dim)
-    word = mask.dtype if isinstance(mask, torch.Tensor) and mask.dtype == torch.uint32 else torch.int32
-    return (T, _dptr(q, "q", rows, d.torch_dtype, dev),
-            (_dptr(seq_lens, "seq_lens", (d.batch,), torch.int32, dev), _dptr(n_new, "n_new", (d.batch,), torch.int32, dev, True),
-             _dptr(mask, "mask", (d.batch, T, -(-T // 32)), word, dev, True)), _dptr(out, "out", rows, d.torch_dtype, dev))
+    _check(_serving.window_prefill(dims, q, K, V, seq_lens, window, n_sink, scale, out, ws, _handle(stream)),
+           "hata_window_prefill")
 
 
 def hata_tree_attention(dims: Dims, q, K, V, seq_lens, n_new, mask, scale, out, ws, stream=None):
     """Attention of the drafted tokens q ([B][Hq][n_tok][d]) over a cache that holds them: mask [B][n_tok][words]
     (int32 or uint32 bits: which drafted tokens each one sees), or None for a chain."""
-    dev = _device()
-    T, pq, seqs, po = _tree_args(dims, dev, q, seq_lens, n_new, mask, out)
-    _check(
-        lib.hata_tree_attention(ctypes.byref(dims), T, pq, *_cache_args(dims, dev, K, V), *seqs, float(scale), po, *_ws(ws, dev),
-                                _stream(stream)),
-        "hata_tree_attention")
+    _check(_serving.tree_attention(dims, q, K, V, None, 0, seq_lens, n_new, mask, scale, out, ws, _handle(stream), False),
+           "hata_tree_attention")
 
 
 def hata_tree_attention_paged(dims: Dims, q, K_pool, V_pool, block_table, block_size, seq_lens, n_new, mask, scale,
                               out, ws, stream=None):
     """hata_tree_attention over paged pools."""
-    dev = _device()
-    T, pq, seqs, po = _tree_args(dims, dev, q, seq_lens, n_new, mask, out)
-    _check(
-        lib.hata_tree_attention_paged(ctypes.byref(dims), T, pq,
-                                      *_pool_args(dims, dev, K_pool, V_pool, block_table, block_size), *seqs, float(scale),
-                                      po, *_ws(ws, dev), _stream(stream)),
-        "hata_tree_attention_paged")
+    _check(_serving.tree_attention(dims, q, K_pool, V_pool, block_table, block_size, seq_lens, n_new, mask, scale, out, ws,
+                                   _handle(stream), True), "hata_tree_attention_paged")
 
 
 def hata_pages_workspace_size(dims: Dims) -> int:
@@ -709,77 +580,31 @@ def hata_pages_workspace_size(dims: Dims) -> int:
     return n.value
 
 
-def _table_args(d, dev, block_table, block_size):
-    bs = int(block_size)
-    return _dptr(block_table, "block_table", (d.batch, -(-d.max_seq // bs) if bs > 0 else 0), torch.int32, dev), bs
-
-
 def hata_pages_fork(dims: Dims, parent, block_table, block_size, seq_lens, ref_count, ws, stream=None):
     """Row b of the table takes the pages and the length of row parent[b] (< 0 or b: unchanged); pages are shared."""
-    d = dims
-    dev = _device()
-    table, bs = _table_args(d, dev, block_table, block_size)
-    n_blocks = ref_count.numel() if isinstance(ref_count, torch.Tensor) else 0
-    _check(
-        lib.hata_pages_fork(
-            ctypes.byref(d), _dptr(parent, "parent", (d.batch,), torch.int32, dev), table, bs, n_blocks,
-            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32, dev),
-            _dptr(ref_count, "ref_count", (n_blocks,), torch.int32, dev), *_ws(ws, dev), _stream(stream)),
-        "hata_pages_fork")
-
-
-def _codes_args(codes, d, dev, lead):
-    return _dptr(codes, "codes", d.code_shape(*lead), _codes_dtype(codes, d), dev, True)
+    _check(_serving.pages_fork(dims, parent, block_table, block_size, seq_lens, ref_count, ws, _handle(stream)),
+           "hata_pages_fork")
 
 
 def hata_pages_resize(dims: Dims, new_lens, K_pool, V_pool, codes_pool, block_table, block_size, seq_lens, ref_count,
                       ws, stream=None):
     """Every sequence to new_lens[b]: pages freed, a shared partial last page copied before it grows, pages added."""
-    d = dims
-    dev = _device()
-    pk, pv, table, bs, n_blocks = _pool_args(d, dev, K_pool, V_pool, block_table, block_size)
-    _check(
-        lib.hata_pages_resize(
-            ctypes.byref(d), _dptr(new_lens, "new_lens", (d.batch,), torch.int32, dev), pk, pv,
-            _codes_args(codes_pool, d, dev, (n_blocks, d.n_kv_heads, bs)), table, bs, n_blocks,
-            _dptr(seq_lens, "seq_lens", (d.batch,), torch.int32, dev),
-            _dptr(ref_count, "ref_count", (n_blocks,), torch.int32, dev), *_ws(ws, dev), _stream(stream)),
-        "hata_pages_resize")
-
-
-def _keep_args(d, dev, keep, n_keep, n_new, seq_lens):
-    if not isinstance(keep, torch.Tensor) or keep.dim() != 2:
-        raise ValueError("keep must be a tensor [B][n_tok]")
-    T, b = keep.shape[1], (d.batch,)
-    return (T, _dptr(keep, "keep", (d.batch, T), torch.int32, dev), _dptr(n_keep, "n_keep", b, torch.int32, dev),
-            _dptr(n_new, "n_new", b, torch.int32, dev, True), _dptr(seq_lens, "seq_lens", b, torch.int32, dev))
+    _check(_serving.pages_resize(dims, new_lens, K_pool, V_pool, codes_pool, block_table, block_size, seq_lens, ref_count, ws,
+                                 _handle(stream)), "hata_pages_resize")
 
 
 def hata_compact_kv(dims: Dims, keep, n_keep, n_new, seq_lens, K, V, codes, new_lens, ws, stream=None):
     """Of the newest n_new[b] tokens keep rows keep[b][:n_keep[b]] (ascending), moved to the front of them in K, V and
     codes (or None); new_lens[b] (or None) receives the length that is left."""
-    d = dims
-    dev = _device()
-    _check(
-        lib.hata_compact_kv(
-            ctypes.byref(d), *_keep_args(d, dev, keep, n_keep, n_new, seq_lens), *_cache_args(d, dev, K, V),
-            _codes_args(codes, d, dev, (d.batch, d.n_kv_heads, d.max_seq)),
-            _dptr(new_lens, "new_lens", (d.batch,), torch.int32, dev, True), *_ws(ws, dev), _stream(stream)),
-        "hata_compact_kv")
+    _check(_serving.compact_kv(dims, keep, n_keep, n_new, seq_lens, K, V, codes, None, 0, new_lens, ws, _handle(stream), False),
+           "hata_compact_kv")
 
 
 def hata_compact_kv_paged(dims: Dims, keep, n_keep, n_new, seq_lens, K_pool, V_pool, codes_pool, block_table,
                           block_size, new_lens, ws, stream=None):
     """hata_compact_kv over paged pools."""
-    d = dims
-    dev = _device()
-    pk, pv, table, bs, n_blocks = _pool_args(d, dev, K_pool, V_pool, block_table, block_size)
-    _check(
-        lib.hata_compact_kv_paged(
-            ctypes.byref(d), *_keep_args(d, dev, keep, n_keep, n_new, seq_lens), pk, pv,
-            _codes_args(codes_pool, d, dev, (n_blocks, d.n_kv_heads, bs)), table, bs, n_blocks,
-            _dptr(new_lens, "new_lens", (d.batch,), torch.int32, dev, True), *_ws(ws, dev), _stream(stream)),
-        "hata_compact_kv_paged")
+    _check(_serving.compact_kv(dims, keep, n_keep, n_new, seq_lens, K_pool, V_pool, codes_pool, block_table, block_size,
+                               new_lens, ws, _handle(stream), True), "hata_compact_kv_paged")
 
 
 def hata_read_device_status(ws, stream=None) -> int:

@@ -6,7 +6,9 @@
 
 Compiles every hash_aware_top_b200/csrc/*.cu to an object under _build/ and
 links them into hash_aware_top_b200/libhata.so (CUDA runtime linked
-statically).  Rebuilds only when a source or header is newer than the library.
+statically), then the benchmark's loop (libhata_e2e.so) and the native half of
+the binding (_serving.so, g++ against the headers of the installed torch).
+Rebuilds only when a source or header is newer than the library.
 """
 from __future__ import annotations
 
@@ -17,6 +19,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -56,6 +59,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     srcs = _sources()
     hdrs = _headers()
     if not force and not _stale(LIB, srcs + hdrs) and not _stale(E2E_LIB, [E2E_SRC, LIB]):
+        build_binding(False, verbose)
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -85,6 +89,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     build_e2e(cc, flags, verbose)
+    build_binding(force, verbose)
     return LIB
 
 
@@ -104,6 +109,32 @@ def build_e2e(cc, flags, verbose=False):
         if r.returncode != 0:
             raise RuntimeError(f"e2e driver build failed:\n{r.stdout}\n{r.stderr}")
     os.replace(E2E_LIB + ".tmp", E2E_LIB)
+
+
+BINDING_SRC = os.path.join(PKG, "binding", "serving.cpp")
+BINDING_LIB = os.path.join(PKG, "_serving.so")
+
+
+def build_binding(force=False, verbose=False):
+    """The native half of the Python binding.  It calls the C ABI, so it is rebuilt when a header changes."""
+    if not force and not _stale(BINDING_LIB, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+        return
+    import torch  # its headers, its ABI
+
+    base = os.path.dirname(torch.__file__)
+    tmp = BINDING_LIB + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(base, "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
+           BINDING_SRC, "-o", tmp, "-L" + PKG, "-lhata", "-L" + os.path.join(base, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding build failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_LIB)
 
 
 def main(argv=None):
