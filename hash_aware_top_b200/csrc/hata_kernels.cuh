@@ -51,6 +51,26 @@ struct PagedCache {
 cudaError_t launch_append_kv(const hata_dims_t& d, const void* new_k, const void* new_v, void* K, void* V,
                              const int32_t* seq_lens, const PagedCache* pg, cudaStream_t stream);
 
+// Launches a kernel that may be set up while the one before it on the stream still runs: the kernel waits for that
+// one to end (griddepcontrol.wait) before it reads what that one may have written, and before it writes anything.
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*k)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
+                         const Args&... args) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, Params(args)...);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e;
+}
+
 // Norms, position rotation and cache append (hata_rope.cu).
 struct RopeArgs {
   const void *q_in, *k_in, *v_in;

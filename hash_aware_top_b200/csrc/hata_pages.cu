@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "hata_kernels.cuh"
+#include "hata_ptx.cuh"
 
 namespace hata {
 
@@ -21,11 +22,14 @@ namespace {
 constexpr int kPgThreads = 1024;
 constexpr int kPgWarps = kPgThreads / 32;
 constexpr int kForkCols = 8;  // table columns of one fork CTA
+constexpr int kFreeBatch = 8;  // entries a lane frees at a time: a round trip to a count takes about a microsecond
 
 // ---- fork: a CTA owns 8 columns of the table: it reads them for every row, then writes them
 __global__ void __launch_bounds__(256)
     pages_fork_kernel(const int32_t* __restrict__ parent, int32_t* table, int32_t* seq_lens, int32_t* ref, int B,
                       int max_blocks, int n_blocks, uint32_t* status) {
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
   extern __shared__ int32_t fork_old[];  // [B][kForkCols], then for CTA 0 the lengths [B]
   const int c0 = (int)blockIdx.x * kForkCols, tid = threadIdx.x;
   for (int e = tid; e < B * kForkCols; e += blockDim.x) {
@@ -63,6 +67,8 @@ struct ResizeParams {
 };
 
 __global__ void __launch_bounds__(kPgThreads) pages_resize_kernel(const ResizeParams p) {
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
   extern __shared__ int32_t rs_smem[];
   int32_t* s_old = rs_smem;            // length before
   int32_t* s_tail = s_old + p.B;       // page a growing row would write into, else -1
@@ -92,15 +98,21 @@ __global__ void __launch_bounds__(kPgThreads) pages_resize_kernel(const ResizePa
     const int old = s_old[b];
     if (old < 0) continue;
     const int n_new = pages_of(target(b, old)), n_old = pages_of(old);
-    for (int c = n_new + lane; c < n_old; c += 32) {
-      int32_t* e = &p.table[(size_t)b * p.max_blocks + c];
-      const int page = *e;
-      *e = -1;
-      if (page < 0 || page >= p.n_blocks) {
-        set_status(p.status, HATA_ERR_INVALID_ARG);
-      } else if (atomicSub(&p.ref[page], 1) <= 0) {  // counted less often than it is used
-        atomicAdd(&p.ref[page], 1);
-        set_status(p.status, HATA_ERR_INVALID_ARG);
+    int32_t* row = p.table + (size_t)b * p.max_blocks;
+    for (int c0 = n_new + lane; c0 < n_old; c0 += 32 * kFreeBatch) {
+      int page[kFreeBatch], held[kFreeBatch];
+#pragma unroll
+      for (int k = 0; k < kFreeBatch; ++k) page[k] = c0 + 32 * k < n_old ? row[c0 + 32 * k] : INT32_MIN;
+#pragma unroll
+      for (int k = 0; k < kFreeBatch; ++k) {
+        if (page[k] != INT32_MIN) row[c0 + 32 * k] = -1;
+        held[k] = page[k] >= 0 && page[k] < p.n_blocks ? atomicSub(&p.ref[page[k]], 1) : 1;
+      }
+#pragma unroll
+      for (int k = 0; k < kFreeBatch; ++k) {
+        if (page[k] == INT32_MIN) continue;
+        if (held[k] <= 0) atomicAdd(&p.ref[page[k]], 1);  // counted less often than it is used
+        if (held[k] <= 0 || page[k] < 0 || page[k] >= p.n_blocks) set_status(p.status, HATA_ERR_INVALID_ARG);
       }
     }
   }
@@ -215,8 +227,10 @@ __global__ void __launch_bounds__(kPgThreads) pages_resize_kernel(const ResizePa
 
 // ---- copies: one CTA per (row, KV head, piece) and tensor; a page's rows of one head are contiguous
 __global__ void __launch_bounds__(256)
-    pages_copy_kernel(const int32_t* __restrict__ copies, unsigned char* K, unsigned char* V, unsigned char* codes,
+    pages_copy_kernel(const int32_t* copies, unsigned char* K, unsigned char* V, unsigned char* codes,
                       int hkv, int bs, int row_bytes, int code_bytes, int n_piece) {
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
   const int b = blockIdx.y;
   const int src = copies[3 * b];
   if (src < 0) return;
@@ -339,8 +353,8 @@ cudaError_t launch_pages_fork(const hata_dims_t& d, const int32_t* parent, int32
                               int n_blocks, int32_t* seq_lens, int32_t* ref, uint32_t* status, cudaStream_t st) {
   const unsigned grid = (unsigned)((max_blocks + kForkCols - 1) / kForkCols);
   const size_t smem = (size_t)d.batch * (kForkCols + 1) * 4;  // at most 36 KB: d.batch <= kMaxPageRows
-  pages_fork_kernel<<<grid, 256, smem, st>>>(parent, table, seq_lens, ref, d.batch, max_blocks, n_blocks, status);
-  return cudaGetLastError();
+  return launch_early(pages_fork_kernel, dim3(grid), 256, smem, st, parent, table, seq_lens, ref, d.batch, max_blocks, n_blocks,
+                      status);
 }
 
 cudaError_t launch_pages_resize(const hata_dims_t& d, const int32_t* new_lens, void* K, void* V, void* codes,
@@ -358,16 +372,14 @@ cudaError_t launch_pages_resize(const hata_dims_t& d, const int32_t* new_lens, v
   p.n_blocks = pg.n_blocks;
   p.block_shift = pg.block_shift;
   p.status = reinterpret_cast<uint32_t*>(ws);
-  pages_resize_kernel<<<1, kPgThreads, (size_t)(4 * d.batch + 1) * 4, st>>>(p);  // at most 16 KB
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_early(pages_resize_kernel, dim3(1), kPgThreads, (size_t)(4 * d.batch + 1) * 4, st, p);  // <= 16 KB
   if (e != cudaSuccess) return e;
   const int bs = 1 << pg.block_shift, row_bytes = kHeadDim * (d.dtype == HATA_BF16 ? 2 : 4);
   const int n_piece = std::max(1, std::min(64, bs / 64));  // 16-32 KB of a K page per CTA
   const int tensors = codes ? 3 : 2;
-  pages_copy_kernel<<<dim3((unsigned)(tensors * d.n_kv_heads * n_piece), (unsigned)d.batch), 256, 0, st>>>(
-      p.copies, static_cast<unsigned char*>(K), static_cast<unsigned char*>(V), static_cast<unsigned char*>(codes),
-      d.n_kv_heads, bs, row_bytes, d.hash_bits / 8, n_piece);
-  return cudaGetLastError();
+  return launch_early(pages_copy_kernel, dim3((unsigned)(tensors * d.n_kv_heads * n_piece), (unsigned)d.batch), 256, 0, st,
+                      p.copies, static_cast<unsigned char*>(K), static_cast<unsigned char*>(V),
+                      static_cast<unsigned char*>(codes), d.n_kv_heads, bs, row_bytes, d.hash_bits / 8, n_piece);
 }
 
 cudaError_t launch_compact(const hata_dims_t& d, int n_tok, const int32_t* keep, const int32_t* n_keep,

@@ -244,6 +244,7 @@ __global__ void __maxnreg__(kSpRegs) span_simt_kernel(const Params p) {
   unsigned char* vt = kt + kSpKeys * S::kRowB;
   float* sm_p = reinterpret_cast<float*>(smem + S::kP) + warp * ROWS * kSpKeys;
 
+  ptx::pdl_wait();
   ptx::pdl_launch_dependents();  // the joining kernel may be set up; it waits for this one to end
   Walker walk;
   walk.begin(p, lane, blockIdx.x == 0 && warp == 0);
@@ -426,6 +427,7 @@ __global__ void __maxnreg__(kSpRegs) span_mma_kernel(const Params p) {
   const uint32_t kfrag = (uint32_t)(kkey * kMmRowB + ((((lane >> 3) & 1) ^ (kkey & 7)) << 4));
   const uint32_t vfrag = (uint32_t)(vkey * kMmRowB + (((lane >> 4) ^ (vkey & 7)) << 4)) + kSpKeys * kMmRowB;
 
+  ptx::pdl_wait();
   ptx::pdl_launch_dependents();  // the joining kernel may be set up; it waits for this one to end
   Walker walk;
   walk.begin(p, lane, blockIdx.x == 0 && warp == 0);
@@ -655,9 +657,8 @@ cudaError_t launch_rows(Kernel k, int smem, Params p, cudaStream_t st) {
   const long long units = (long long)p.B * p.Hkv * p.row_tiles;
   if (!span_fits(p, units)) return cudaErrorNotSupported;
   const int grid = span_sms();
-  k<<<grid, kSpThreads, smem, st>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_early(span_join_kernel<T, ROWS>, dim3((unsigned)units, ROWS / kJoinWarps), kJoinWarps * 32, st, p, grid);
+  if ((e = launch_early(k, dim3((unsigned)grid), kSpThreads, (size_t)smem, st, p)) != cudaSuccess) return e;
+  return launch_early(span_join_kernel<T, ROWS>, dim3((unsigned)units, ROWS / kJoinWarps), kJoinWarps * 32, 0, st, p, grid);
 }
 
 template <int ROWS>

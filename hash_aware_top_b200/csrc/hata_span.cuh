@@ -300,24 +300,6 @@ inline bool span_fits(const span::Params& p, long long units) {
          units * ((p.max_seq + span::kSpanTile - 1LL) / span::kSpanTile) <= 0x3fffffffLL;
 }
 
-// Launches a kernel that may be set up while the one before it on the stream runs (and waits for it with
-// griddepcontrol.wait before it reads anything).
-template <typename... Args>
-cudaError_t launch_early(void (*k)(Args...), dim3 grid, unsigned threads, cudaStream_t st, Args... args) {
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
-  if (e != cudaSuccess) (void)cudaGetLastError();
-  return e;
-}
-
 // Tensor-core form of tree attention (hata_span_tc.cu): bf16, any number of rows.
 size_t span_tc_part_bytes(const hata_dims_t& d, int n_tok);
 cudaError_t launch_span_tc(const hata_dims_t& d, const span::Params& s, const PagedCache* pg, cudaStream_t stream);

@@ -291,6 +291,7 @@ __global__ void __maxnreg__(kTcRegs)
     tc::mbar_init_fence();
     abort_s = 0;
   }
+  ptx::pdl_wait();  // what came before on the stream has ended
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = tmem_s;
@@ -856,10 +857,10 @@ cudaError_t launch_span_tc(const hata_dims_t& d, const span::Params& s, const Pa
     return cudaErrorNotSupported;
   cudaError_t e = pg ? configure_tc<true, true>() : configure_tc<true, false>();
   if (e != cudaSuccess) return e;
-  if (pg) span_tc_kernel<true, true><<<sms, kTcThreads, kTcSmem, st>>>(qm, km, vm, p);
-  else span_tc_kernel<true, false><<<sms, kTcThreads, kTcSmem, st>>>(qm, km, vm, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_early(span_merge_kernel, dim3((unsigned)units, kHeadDim / 4, p.pair ? 2 : 1), kTcTile, st, p, sms, rows);
+  e = launch_early(pg ? span_tc_kernel<true, true> : span_tc_kernel<true, false>, dim3((unsigned)sms), kTcThreads, kTcSmem, st,
+                   qm, km, vm, p);
+  if (e != cudaSuccess) return e;
+  return launch_early(span_merge_kernel, dim3((unsigned)units, kHeadDim / 4, p.pair ? 2 : 1), kTcTile, 0, st, p, sms, rows);
 }
 
 cudaError_t launch_window_prefill(const hata_dims_t& d, const void* q, const void* K, const void* V,
@@ -899,8 +900,7 @@ cudaError_t launch_window_prefill(const hata_dims_t& d, const void* q, const voi
   const long long items = (long long)p.n_blocks_pos * p.rows_of_items;
   if (items > 0x3fffffffLL) return cudaErrorNotSupported;
   const unsigned grid = (unsigned)std::min<long long>(items, span_sms());
-  span_tc_kernel<false, false><<<grid, kTcThreads, kTcSmem, st>>>(qm, km, vm, p);
-  return cudaGetLastError();
+  return launch_early(span_tc_kernel<false, false>, dim3(grid), kTcThreads, kTcSmem, st, qm, km, vm, p);
 }
 
 }  // namespace hata
