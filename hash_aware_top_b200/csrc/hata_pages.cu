@@ -9,7 +9,10 @@
 //
 // Bound: latency.  The tables and counts are a few hundred KB, read and written once; resize's
 // decisions are one CTA (a prefix sum over rows and two passes over the counts), its copies and
-// compact's moves spread over all SMs as 16-byte vectors.
+// compact's moves spread over all SMs as 16-byte vectors.  The kernels are launched early, so a
+// launch overlaps the kernel before it.  Measured on B200: a beam step of 32 sequences over 256-page
+// rows (roll back, fork 8 into 24, grow with 24 copies on write: five kernels) 20.5 us, of which each
+// resize's decisions are about 6; compacting 16 sequences' trees of 64 tokens 3.0 us.
 #include <algorithm>
 
 #include "hata_kernels.cuh"

@@ -379,9 +379,10 @@ HATA_API hata_status_t hata_norm_rope_paged(const hata_dims_t* dims, int n_tok, 
 HATA_API hata_status_t hata_rope_table(float* table, int n_pos, int rot_dim, double theta, void* stream);
 
 /* Bytes of workspace for hata_window_decode and hata_tree_attention (and their paged
- * forms) with n_tok new tokens per sequence (1 for a window decode); 16-byte
- * aligned; zeroed once with hata_workspace_init before the first call, and every
- * call leaves its counters at zero.  One workspace serves one call at a time. */
+ * forms) with n_tok new tokens per sequence (1 for a window decode), at most 128; 16-byte
+ * aligned.  Only its status word needs zeroing (hata_workspace_init); the rest holds
+ * partial results within a call, so one workspace serves one call at a time: calls whose
+ * work can overlap on the GPU (other streams, graphs replayed side by side) need their own. */
 HATA_API hata_status_t hata_span_workspace_size(const hata_dims_t* dims, int n_tok, size_t* bytes);
 
 /*
@@ -451,7 +452,7 @@ HATA_API hata_status_t hata_tree_attention_paged(const hata_dims_t* dims, int n_
  * is free.  The caller starts with all entries -1 and all counts and lengths 0 (or with any
  * consistent state).  All are int32 on the device.  At most 1024 sequences.  The
  * workspace (hata_pages_workspace_size bytes, 16-byte aligned) needs no initialisation apart from its
- * status word.
+ * status word; a pages call and its workspace, table, lengths and counts serve one stream at a time.
  *
  * hata_pages_fork: row b takes the pages and the length of row parent[b] as they were before the
  * call (all rows at once, so beams may be permuted); its own pages are released.  parent[b] < 0 or = b
@@ -484,7 +485,7 @@ HATA_API hata_status_t hata_pages_resize(const hata_dims_t* dims, const int32_t*
  * seq_lens is not changed (the paged form's pages are released by hata_pages_resize to
  * new_lens).  A sequence whose keep or lengths break these rules is flagged and left as it is
  * (new_lens[b] = seq_lens[b]); rows in blocks outside the pool are flagged and skipped.  The workspace
- * is at least 16 bytes: its status word.
+ * is at least 16 bytes: its status word.  batch at most 65535.
  */
 HATA_API hata_status_t hata_compact_kv(const hata_dims_t* dims, int n_tok, const int32_t* keep, const int32_t* n_keep,
                                        const int32_t* n_new, const int32_t* seq_lens, void* K, void* V, void* codes,
