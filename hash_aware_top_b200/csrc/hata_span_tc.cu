@@ -281,6 +281,8 @@ __global__ void __maxnreg__(kTcRegs)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (tc::smem_u32(tc_smem) + 1023u) & ~1023u;
+  // What came before on the stream has ended, before TMEM is taken: its CTAs may need TMEM of this SM.
+  ptx::pdl_wait();
   if (warp == 0) tc::tmem_alloc(&tmem_s, kTcTmemCols);
   if (tid == 256) {
     tc::mbar_init(&q_full, 1);
@@ -300,7 +302,6 @@ __global__ void __maxnreg__(kTcRegs)
     tc::mbar_init_fence();
     abort_s = 0;
   }
-  ptx::pdl_wait();  // what came before on the stream has ended
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = tmem_s;

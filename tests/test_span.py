@@ -270,6 +270,51 @@ def test_tree_bad_lengths_are_flagged_and_left(H):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,Hq", [(1, 4), (6, 4), (40, 4)])
+def test_offsets_past_32_bits(H, T, Hq):
+    """Pages at the end of pools of more than 2^31 elements, and slots at the end of such a contiguous cache."""
+    B, Hkv, bs = 1, 1, 256
+    n = 2**31 // (Hkv * bs * D) + 600
+    K, V = (torch.empty(n, Hkv, bs, D, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    L = 1000
+    d = H.dims_for(B, Hq, Hkv, D, 128, L, "bf16")
+    bt = torch.tensor([[n - 1, n - 3, n - 599, n - 2]], dtype=torch.int32, device="cuda")
+    q = torch.randn(B, Hq, T, D, device="cuda").bfloat16()
+    Kd, Vd = torch.randn(2, L, D, device="cuda").bfloat16().unbind(0)
+    for i in range(4):
+        K[bt[0, i].long(), 0, : min(bs, L - i * bs)] = Kd[i * bs:(i + 1) * bs]
+        V[bt[0, i].long(), 0, : min(bs, L - i * bs)] = Vd[i * bs:(i + 1) * bs]
+    out, ws = torch.zeros_like(q), torch.zeros(H.hata_span_workspace_size(d, T), dtype=torch.uint8, device="cuda")
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    H.hata_tree_attention_paged(d, q, K, V, bt, bs, lens, None, None, 0.0, out, ws)
+    sees = torch.arange(L, device="cuda")[None] <= L - T + torch.arange(T, device="cuda")[:, None]
+    for h in range(Hq):
+        want, absv, qk = attend(q[0, h], Kd, Vd, sees)
+        close(out[0, h], want, absv, qk, L, torch.bfloat16)
+    # the same memory as one contiguous cache of 2^24 slots and more
+    S = n * bs
+    K, V = K.view(1, 1, S, D), V.view(1, 1, S, D)
+    K[0, 0, S - L:], V[0, 0, S - L:] = Kd, Vd
+    K[0, 0, :5], V[0, 0, :5] = Kd[:5], Vd[:5]
+    d = H.dims_for(B, Hq, Hkv, D, 128, S, "bf16")
+    lens = torch.tensor([S], dtype=torch.int32, device="cuda")
+    out = torch.zeros(B, Hq, D, device="cuda", dtype=torch.bfloat16)
+    ws = torch.zeros(H.hata_span_workspace_size(d, 1), dtype=torch.uint8, device="cuda")
+    H.hata_window_decode(d, q[:, :, 0].contiguous(), K, V, lens, L, 5, 0.0, out, ws)
+    for h in range(Hq):
+        want, absv, qk = attend(q[0, h, :1], torch.cat([Kd[:5], Kd]), torch.cat([Vd[:5], Vd]), torch.ones(1, L + 5, dtype=torch.bool, device="cuda"))
+        close(out[0, h][None], want, absv, qk, L + 5, torch.bfloat16)
+    x = torch.randn(1, T, Hq + 2, D, device="cuda").bfloat16()
+    q_out = torch.zeros(1, Hq, T, D, device="cuda", dtype=torch.bfloat16)
+    H.hata_norm_rope(d, x[:, :, :Hq], x[:, :, Hq:Hq + 1], x[:, :, Hq + 1:], None, None, 1e-6, None, False, None, None, lens, q_out, K, V, ws)
+    assert torch.equal(K[0, 0, S - T:], x[0, :, Hq]) and torch.equal(V[0, 0, S - T:], x[0, :, Hq + 1])
+    keep = torch.arange(T, dtype=torch.int32, device="cuda")[None].contiguous()
+    keep[0, 0] = T - 1
+    H.hata_compact_kv(d, keep, torch.ones(1, dtype=torch.int32, device="cuda"), None, lens, K, V, None, None, ws)
+    assert torch.equal(K[0, 0, S - T], x[0, T - 1, Hq]) and H.hata_read_device_status(ws) == 0
+
+
+@pytest.mark.gpu
 def test_captured_and_replayed(H):
     """A captured window decode and tree attention give the eager results, replayed with other inputs."""
     c = Cache(H, torch.bfloat16, 2, 8, 2, 500, 16, 5)
