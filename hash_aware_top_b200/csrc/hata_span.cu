@@ -82,11 +82,11 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* out, float4
 }
 
 // The weights that bring the warps' outputs of each row to one maximum: sm_m, sm_l [n][ROWS] (maximum, sum) become
-// sm_m = 2^(m - M) and, for row r, (M, sum of l 2^(m - M)) in row_m, row_l.  A warp per row; all threads.
+// sm_m = 2^(m - M) and, for row r < rows, (M, sum of l 2^(m - M)) in row_m, row_l.  A warp per row; all threads.
 template <int ROWS>
-__device__ __forceinline__ void join_weights(float* sm_m, const float* sm_l, int n, float* row_m, float* row_l) {
+__device__ __forceinline__ void join_weights(float* sm_m, const float* sm_l, int n, int rows, float* row_m, float* row_l) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int r = warp; r < ROWS; r += kSpWarps) {
+  for (int r = warp; r < rows; r += kSpWarps) {
     float M = -INFINITY;
     for (int i = lane; i < n; i += 32) M = fmaxf(M, sm_m[i * ROWS + r]);
 #pragma unroll
@@ -122,11 +122,11 @@ template <typename T, int ROWS>
 __device__ __forceinline__ void finish_unit(const Params& p, float* sm_m, float* sm_l, const float* sm_o,
                                             const Piece& pc, int g, int rt) {
   __shared__ float row_m[ROWS], row_l[ROWS];
-  const int tid = threadIdx.x, r0 = rt * ROWS;
+  const int tid = threadIdx.x, r0 = rt * ROWS, rows = min(ROWS, p.R - r0);
   T* out = static_cast<T*>(p.out) + (((size_t)pc.b * p.Hq + (size_t)g * p.G) * p.T + r0) * kHeadDim;
   float* part = part_of<ROWS>(p, pc.slot);
-  join_weights<ROWS>(sm_m, sm_l, kSpWarps, row_m, row_l);
-  for (int e = tid; e < ROWS * kHeadDim / 4; e += kSpThreads) {
+  join_weights<ROWS>(sm_m, sm_l, kSpWarps, rows, row_m, row_l);
+  for (int e = tid; e < rows * (kHeadDim / 4); e += kSpThreads) {
     const int r = e / (kHeadDim / 4), c = e % (kHeadDim / 4);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -140,13 +140,13 @@ __device__ __forceinline__ void finish_unit(const Params& p, float* sm_m, float*
     }
     if (pc.whole) {
       const float l = row_l[r], inv = l == 0.f ? 0.f : 1.f / l;
-      if (r0 + r < p.R && (r0 + r) % p.T < pc.seq.n_b)
+      if ((r0 + r) % p.T < pc.seq.n_b)
         store4<T>(out + 4 * e, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     } else {
       reinterpret_cast<float4*>(part + 2 * ROWS)[e] = o;
     }
   }
-  if (!pc.whole && tid < ROWS) {
+  if (!pc.whole && tid < rows) {
     part[tid] = row_m[tid];
     part[ROWS + tid] = row_l[tid];
   }
@@ -256,7 +256,7 @@ __global__ void __maxnreg__(kSpRegs) span_simt_kernel(const Params p) {
   const int key = lane & 15, half = lane >> 4;
   Piece pc;
   while (walk.next(p, pc)) {
-    const int b = pc.b, g = pc.in_seq % p.Hkv, rt = pc.in_seq / p.Hkv, j0 = pc.j0, j1 = pc.j1;
+    const int rt = p.row_tiles == 1 ? 0 : pc.in_seq / p.Hkv, b = pc.b, g = pc.in_seq - rt * p.Hkv, j0 = pc.j0, j1 = pc.j1;
     const Seq& sq = pc.seq;
     const int r0 = rt * ROWS;
     auto first_slot = [&](int j) {
@@ -438,7 +438,7 @@ __global__ void __maxnreg__(kSpRegs) span_mma_kernel(const Params p) {
   walk.begin(p, lane, blockIdx.x == 0 && warp == 0);
   Piece pc;
   while (walk.next(p, pc)) {
-    const int b = pc.b, g = pc.in_seq % p.Hkv, rt = pc.in_seq / p.Hkv, j0 = pc.j0, j1 = pc.j1;
+    const int rt = p.row_tiles == 1 ? 0 : pc.in_seq / p.Hkv, b = pc.b, g = pc.in_seq - rt * p.Hkv, j0 = pc.j0, j1 = pc.j1;
     const Seq& sq = pc.seq;
     const int r0 = rt * ROWS;
     auto first_slot = [&](int j) {
@@ -620,6 +620,7 @@ __global__ void __maxnreg__(kSpRegs) span_mma_kernel(const Params p) {
         float sum = l[mt][h];
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (r0 + r >= p.R) continue;
         if (cq == 0) {
           sm_m[warp * ROWS + r] = m[mt][h];
           sm_l[warp * ROWS + r] = sum;

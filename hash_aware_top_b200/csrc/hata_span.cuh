@@ -91,11 +91,20 @@ struct Split {
   bool aligned;
 };
 
+// a / b.  A 32-bit division takes over a hundred cycles, and every CTA does several before it can load anything; below
+// 2^22 the quotient of the floats is off by one at most.
+__device__ __forceinline__ unsigned quotient(unsigned a, unsigned b) {
+  if (a >= (1u << 22)) return a / b;
+  const unsigned q = __float2uint_rz(__fdividef((float)a, (float)b));
+  const int r = (int)(a - q * b);
+  return r < 0 ? q - 1 : (unsigned)r >= b ? q + 1 : q;
+}
+
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
 // aligned: CTAs of a unit.  32-bit: a unit has at most 2^24 tiles, a GPU at most 255 SMs (both checked on the host).
 __device__ __forceinline__ int ctas_of(const Split& sp, int tiles, int grid) {
-  return tiles == 0 ? 0 : min(tiles, 1 + (int)((unsigned)tiles * (unsigned)(grid - sp.units) / (unsigned)sp.total));
+  return tiles == 0 ? 0 : min(tiles, 1 + (int)quotient((unsigned)tiles * (unsigned)(grid - sp.units), (unsigned)sp.total));
 }
 
 // Tiles of each unit of sequence b0 + lane.
@@ -120,13 +129,13 @@ __device__ __forceinline__ Split split_of(const Params& p, int lane, int grid, b
     sp.total += warp_sum(n) * upt;
     sp.units += __popc(__ballot_sync(0xffffffffu, n > 0)) * upt;
   }
-  sp.per = max(1, (int)((unsigned)(sp.total + grid - 1) / (unsigned)grid));
+  sp.per = max(1, (int)quotient((unsigned)(sp.total + grid - 1), (unsigned)grid));
   sp.aligned = false;
   if (sp.units > 0 && sp.units <= grid) {
     int longest = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int tiles = tiles_at(p, sp, b0, lane), k = ctas_of(sp, tiles, grid);
-      longest = max(longest, __reduce_max_sync(0xffffffffu, k ? (int)((unsigned)(tiles + k - 1) / (unsigned)k) : 0));
+      longest = max(longest, __reduce_max_sync(0xffffffffu, k ? (int)quotient((unsigned)(tiles + k - 1), (unsigned)k) : 0));
     }
     sp.aligned = longest <= sp.per + kSwitchTiles;
   }
@@ -198,12 +207,13 @@ struct Walker {
     }
     seq = seq_of(p, b);
     if (sp.aligned) {
-      const unsigned k = (unsigned)ctas_of(sp, seq.tiles, grid), part = (unsigned)(at - base) % k;
+      const unsigned k = (unsigned)ctas_of(sp, seq.tiles, grid), unit = quotient((unsigned)(at - base), k);
+      const unsigned part = (unsigned)(at - base) - unit * k;
       only.b = b;
-      only.in_seq = (int)((unsigned)(at - base) / k);
+      only.in_seq = (int)unit;
       only.seq = seq;
-      only.j0 = (int)((unsigned)seq.tiles * part / k);
-      only.j1 = (int)((unsigned)seq.tiles * (part + 1) / k);
+      only.j0 = (int)quotient((unsigned)seq.tiles * part, k);
+      only.j1 = (int)quotient((unsigned)seq.tiles * (part + 1), k);
       only.cta = cta;
       only.whole = k == 1;
       only.slot = 2 * cta;
@@ -226,7 +236,7 @@ struct Walker {
     }
     s.b = b;
     s.seq = seq;
-    s.in_seq = (at - base) / seq.tiles;
+    s.in_seq = (int)quotient((unsigned)(at - base), (unsigned)seq.tiles);
     const int u0 = base + s.in_seq * seq.tiles;
     s.j0 = at - u0;
     s.j1 = min(end - u0, seq.tiles);
