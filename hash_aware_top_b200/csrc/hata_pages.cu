@@ -8,12 +8,14 @@
 // there is no list of free pages to keep, and the result does not depend on the order of threads.
 //
 // Bound: latency.  The tables and counts are a few hundred KB, read and written once; resize's
-// decisions are one CTA (a prefix sum over rows and two passes over the counts), its copies and
+// decisions are one CTA (a prefix sum over rows and two passes over the counts, kept in shared memory), its copies and
 // compact's moves spread over all SMs as 16-byte vectors.  The kernels are launched early, so a
 // launch overlaps the kernel before it.  Measured on B200: a beam step of 32 sequences over 256-page
 // rows (roll back, fork 8 into 24, grow with 24 copies on write: five kernels) 20.5 us, of which each
 // resize's decisions are about 6; compacting 16 sequences' trees of 64 tokens 3.0 us.
 #include <algorithm>
+#include <map>
+#include <mutex>
 
 #include "hata_kernels.cuh"
 #include "hata_ptx.cuh"
@@ -69,38 +71,64 @@ struct ResizeParams {
   uint32_t* status;
 };
 
+// LOCAL: the counts are brought into shared memory first and written back at the end.  Freeing the 4800 entries of 24 rows
+// takes 4800 atomics, at one SM's rate of about one scattered atomic per cycle and 1.7 cycles each 4 us in L2.  Pools whose
+// counts do not fit (about 50,000 pages) do it there.
+template <bool LOCAL>
 __global__ void __launch_bounds__(kPgThreads) pages_resize_kernel(const ResizeParams p) {
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   extern __shared__ int32_t rs_smem[];
-  int32_t* s_old = rs_smem;            // length before
-  int32_t* s_tail = s_old + p.B;       // page a growing row would write into, else -1
-  int32_t* s_first = s_tail + p.B;     // first column that gets a page
-  int32_t* s_pre = s_first + p.B;      // pages needed by earlier rows; [B]: by all
-  __shared__ int32_t warp_sum[kPgWarps];
-  __shared__ int32_t s_total;
+  int32_t* s_old = rs_smem;         // length before, -1: the row stays out of it
+  int32_t* s_new = s_old + p.B;     // length after
+  int32_t* s_tail = s_new + p.B;    // page a growing row would write into, else -1
+  int32_t* s_first = s_tail + p.B;  // first column that gets a page
+  int32_t* s_pre = s_first + p.B;   // pages needed by earlier rows; [B]: by all
+  int32_t* s_ref = s_pre + p.B + 1;  // LOCAL: the counts
+  __shared__ int32_t scan_sum[kPgWarps], free_sum[kPgWarps];
+  __shared__ int32_t s_free;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.B;
   const int bs = 1 << p.block_shift;
   auto pages_of = [&](int len) { return (int)(((long long)len + bs - 1) >> p.block_shift); };
-  // a row whose old or new length lies outside [0, max_seq] stays as it is
-  auto target = [&](int b, int old) {
-    const int nw = p.new_lens[b];
-    return (nw < 0 || nw > p.max_seq) ? old : nw;
+  auto count = [&](int q) -> int {
+    if constexpr (LOCAL) return s_ref[q];
+    else return __ldcg(&p.ref[q]);
   };
+  auto add = [&](int q, int n) -> int {  // the count before
+    if constexpr (LOCAL) return atomicAdd(&s_ref[q], n);
+    else return atomicAdd(&p.ref[q], n);
+  };
+  if constexpr (LOCAL) {
+#pragma unroll 8
+    for (int q = tid; q < p.n_blocks; q += kPgThreads) s_ref[q] = p.ref[q];
+  }
   for (int b = tid; b < B; b += kPgThreads) {
     const int old = p.seq_lens[b], nw = p.new_lens[b];
-    const bool ok = old >= 0 && old <= p.max_seq;
-    if (!ok || nw < 0 || nw > p.max_seq) set_status(p.status, HATA_ERR_INVALID_ARG);
+    const bool ok = old >= 0 && old <= p.max_seq, ok_new = nw >= 0 && nw <= p.max_seq;
+    if (!ok || !ok_new) set_status(p.status, HATA_ERR_INVALID_ARG);
     s_old[b] = ok ? old : -1;
-    s_tail[b] = -1;
+    s_new[b] = ok_new ? nw : old;  // a new length out of range leaves the row as it is
     p.copies[3 * b] = -1;
   }
   __syncthreads();
+  // the last pages of growing rows that are partly filled
+  for (int b = tid; b < B; b += kPgThreads) {
+    const int old = s_old[b];
+    int tail = -1;
+    if (old >= 0 && s_new[b] > old && (old & (bs - 1))) {
+      tail = p.table[(size_t)b * p.max_blocks + pages_of(old) - 1];
+      if (tail < 0 || tail >= p.n_blocks) {
+        tail = -1;
+        set_status(p.status, HATA_ERR_INVALID_ARG);
+      }
+    }
+    s_tail[b] = tail;
+  }
   // frees: a warp per row
   for (int b = warp; b < B; b += kPgWarps) {
     const int old = s_old[b];
     if (old < 0) continue;
-    const int n_new = pages_of(target(b, old)), n_old = pages_of(old);
+    const int n_new = pages_of(s_new[b]), n_old = pages_of(old);
     int32_t* row = p.table + (size_t)b * p.max_blocks;
     for (int c0 = n_new + lane; c0 < n_old; c0 += 32 * kFreeBatch) {
       int page[kFreeBatch], held[kFreeBatch];
@@ -109,41 +137,38 @@ __global__ void __launch_bounds__(kPgThreads) pages_resize_kernel(const ResizePa
 #pragma unroll
       for (int k = 0; k < kFreeBatch; ++k) {
         if (page[k] != INT32_MIN) row[c0 + 32 * k] = -1;
-        held[k] = page[k] >= 0 && page[k] < p.n_blocks ? atomicSub(&p.ref[page[k]], 1) : 1;
+        held[k] = page[k] >= 0 && page[k] < p.n_blocks ? add(page[k], -1) : 1;
       }
 #pragma unroll
       for (int k = 0; k < kFreeBatch; ++k) {
         if (page[k] == INT32_MIN) continue;
-        if (held[k] <= 0) atomicAdd(&p.ref[page[k]], 1);  // counted less often than it is used
+        if (held[k] <= 0) add(page[k], 1);  // counted less often than it is used
         if (held[k] <= 0 || page[k] < 0 || page[k] >= p.n_blocks) set_status(p.status, HATA_ERR_INVALID_ARG);
       }
     }
   }
   __syncthreads();
-  // growing rows whose last page is partly filled and shared
-  for (int b = tid; b < B; b += kPgThreads) {
-    const int old = s_old[b];
-    if (old < 0 || target(b, old) <= old || !(old & (bs - 1))) continue;
-    const int page = p.table[(size_t)b * p.max_blocks + pages_of(old) - 1];
-    if (page >= 0 && page < p.n_blocks) s_tail[b] = page;
-    else set_status(p.status, HATA_ERR_INVALID_ARG);
-  }
-  __syncthreads();
+  // each warp counts the free pages of its share of them
+  const int per = ((p.n_blocks + kPgWarps - 1) / kPgWarps + 31) / 32 * 32;
+  const int p0 = min(p.n_blocks, warp * per), p1 = min(p.n_blocks, p0 + per);
+  int mine = 0;
+#pragma unroll 8
+  for (int q = p0 + lane; q < p1; q += 32) mine += count(q) == 0;
   // needs: of the rows that share a tail page and grow, the earlier ones copy it and, when nobody else holds
   // it, the last one keeps it (what rows handled one after another would do)
   for (int b = tid; b < B; b += kPgThreads) {
     const int old = s_old[b];
     int need = 0, first = 0;
     if (old >= 0) {
-      const int nw = target(b, old), n_old = pages_of(old);
+      const int nw = s_new[b], n_old = pages_of(old);
       int copy = 0;
       if (nw > old) {
         if (s_tail[b] >= 0) {
-          const int held = __ldcg(&p.ref[s_tail[b]]);
+          const int held = count(s_tail[b]);
           if (held > 1) {
-            int before = 0;
-            for (int o = 0; o < b; ++o) before += s_tail[o] == s_tail[b];
-            copy = held - before > 1;
+            int earlier = 0;
+            for (int o = 0; o < b; ++o) earlier += s_tail[o] == s_tail[b];
+            copy = held - earlier > 1;
           }
         }
         need = pages_of(nw) - n_old + copy;
@@ -153,48 +178,39 @@ __global__ void __launch_bounds__(kPgThreads) pages_resize_kernel(const ResizePa
     s_first[b] = first;
     s_pre[b] = need;
   }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) free_sum[warp] = mine;
   __syncthreads();
-  // exclusive prefix over rows
+  // exclusive prefix of the needs over rows
   int carry = 0;
   for (int b0 = 0; b0 < B; b0 += kPgThreads) {
     const int v = b0 + tid < B ? s_pre[b0 + tid] : 0;
     int tot = 0;
-    const int x = block_exclusive_scan<kPgThreads>(v, warp_sum, &tot);
+    const int x = block_exclusive_scan<kPgThreads>(v, scan_sum, &tot);
     if (b0 + tid < B) s_pre[b0 + tid] = carry + x;
     carry += tot;
   }
   if (tid == 0) s_pre[B] = carry;
   const int total = carry;
-  // free pages: each warp counts its share of the pages, then hands out the free ones of its share
-  const int per = ((p.n_blocks + kPgWarps - 1) / kPgWarps + 31) / 32 * 32;
-  const int p0 = min(p.n_blocks, warp * per), p1 = min(p.n_blocks, p0 + per);
-  int mine = 0;
-  if (total > 0) {
-#pragma unroll 8
-    for (int q = p0 + lane; q < p1; q += 32) mine += __ldcg(&p.ref[q]) == 0;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) warp_sum[warp] = mine;
-  __syncthreads();
   if (warp == 0) {
-    int x = warp_sum[lane];
+    int x = free_sum[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) s_total = x;
-    warp_sum[lane] = x;
+    if (lane == 31) s_free = x;
+    free_sum[lane] = x;
   }
   __syncthreads();
-  const bool enough = s_total >= total;
+  const bool enough = s_free >= total;
   if (!enough && tid == 0) set_status(p.status, HATA_ERR_NO_PAGES);
   if (enough && total > 0) {
-    int rank = warp_sum[warp] - mine;  // free pages before this warp's share
+    int rank = free_sum[warp] - mine;  // free pages before this warp's share
     for (int q0 = p0; q0 < p1 && rank < total; q0 += 32) {
       const int q = q0 + lane;
-      const bool is_free = q < p1 && __ldcg(&p.ref[q]) == 0;
+      const bool is_free = q < p1 && count(q) == 0;
       const unsigned m = __ballot_sync(0xffffffffu, is_free);
       const int r = rank + __popc(m & ((1u << lane) - 1u));
       if (is_free && r < total) {
@@ -205,27 +221,45 @@ __global__ void __launch_bounds__(kPgThreads) pages_resize_kernel(const ResizePa
           else hi = mid;
         }
         p.table[(size_t)lo * p.max_blocks + s_first[lo] + (r - s_pre[lo])] = q;
-        p.ref[q] = 1;
+        add(q, 1);
+        if (r == s_pre[lo] && s_first[lo] < pages_of(s_old[lo])) {  // takes the place of a shared last page
+          p.copies[3 * lo + 1] = q;
+          p.copies[3 * lo + 2] = s_old[lo] & (bs - 1);
+          p.copies[3 * lo] = s_tail[lo];
+        }
       }
       rank += __popc(m);
     }
   }
   __syncthreads();
   for (int b = tid; b < B; b += kPgThreads) {
-    const int old = s_old[b];
-    if (old < 0) continue;
-    const int nw = target(b, old), n_old = pages_of(old);
-    if (nw > old) {
-      if (!enough) continue;  // no row grows
-      if (s_first[b] < n_old) {
-        p.copies[3 * b + 1] = p.table[(size_t)b * p.max_blocks + n_old - 1];
-        p.copies[3 * b + 2] = old & (bs - 1);
-        p.copies[3 * b] = s_tail[b];
-        atomicSub(&p.ref[s_tail[b]], 1);
-      }
-    }
+    const int old = s_old[b], nw = s_new[b];
+    if (old < 0 || (nw > old && !enough)) continue;  // too few pages: no row grows
+    if (nw > old && s_first[b] < pages_of(old)) add(s_tail[b], -1);
     p.seq_lens[b] = nw;
   }
+  if constexpr (LOCAL) {
+    __syncthreads();
+#pragma unroll 8
+    for (int q = tid; q < p.n_blocks; q += kPgThreads) p.ref[q] = s_ref[q];
+  }
+}
+
+// Shared memory that counts may take, and the kernel's attribute for it, set once per device under a mutex.
+constexpr size_t kLocalBytes = 220 * 1024;
+cudaError_t configure_local() {
+  static std::mutex mu;
+  static std::map<int, cudaError_t> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  auto it = done.find(dev);
+  if (it != done.end()) return it->second;
+  e = cudaFuncSetAttribute(pages_resize_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLocalBytes);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  done[dev] = e;
+  return e;
 }
 
 // ---- copies: one CTA per (row, KV head, piece) and tensor; a page's rows of one head are contiguous
@@ -375,7 +409,14 @@ cudaError_t launch_pages_resize(const hata_dims_t& d, const int32_t* new_lens, v
   p.n_blocks = pg.n_blocks;
   p.block_shift = pg.block_shift;
   p.status = reinterpret_cast<uint32_t*>(ws);
-  cudaError_t e = launch_early(pages_resize_kernel, dim3(1), kPgThreads, (size_t)(4 * d.batch + 1) * 4, st, p);  // <= 16 KB
+  const size_t rows = (size_t)(5 * d.batch + 1) * 4, local = rows + (size_t)pg.n_blocks * 4;
+  cudaError_t e;
+  if (local <= kLocalBytes) {
+    if ((e = configure_local()) != cudaSuccess) return e;
+    e = launch_early(pages_resize_kernel<true>, dim3(1), kPgThreads, local, st, p);
+  } else {
+    e = launch_early(pages_resize_kernel<false>, dim3(1), kPgThreads, rows, st, p);  // at most 21 KB
+  }
   if (e != cudaSuccess) return e;
   const int bs = 1 << pg.block_shift, row_bytes = kHeadDim * (d.dtype == HATA_BF16 ? 2 : 4);
   const int n_piece = std::max(1, std::min(64, bs / 64));  // 16-32 KB of a K page per CTA

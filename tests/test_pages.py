@@ -137,6 +137,27 @@ def test_random_steps_follow_the_model(H, B, n_blocks, bs, max_seq, r, dtype):
 
 
 @pytest.mark.gpu
+def test_a_pool_whose_counts_do_not_fit_shared_memory(H):
+    """70,000 pages: the counts stay in global memory."""
+    rng = np.random.default_rng(5)
+    B, n_blocks = 6, 70000
+    c = Cache(H, B, 8, 16, 4000, Hkv=1, codes=False)
+    c.K = torch.zeros(n_blocks, 1, 16, D, device="cuda", dtype=torch.bfloat16)
+    c.V, c.ref = c.K.clone(), torch.zeros(n_blocks, dtype=torch.int32, device="cuda")
+    m = Model(B, n_blocks, 16, 4000)
+    for step in range(6):
+        if step % 3 == 1:
+            parent = rng.integers(-1, B, B).tolist()
+            c.fork(parent), m.fork(parent)
+        else:
+            new = [int(x) for x in rng.integers(0, 4001, B)]
+            c.resize(new)
+            assert m.resize(new) is not None
+        assert c.status() == 0
+        c.same_as(m)
+
+
+@pytest.mark.gpu
 def test_growing_sharers_copy_and_the_last_keeps(H):
     c, m = Cache(H, 4, 12, 16, 100), Model(4, 12, 16, 100)
     for step in ([20, 0, 0, 0], "fork", [21, 25, 21, 40]):
