@@ -13,7 +13,8 @@
 //
 // The two streams take
 //   * prefill: 256 rows = P heads of one group x 256 / P positions, P the largest power of two in G (at most
-//     16), so a window's ragged ends cost 256 / P rows, not 256;
+//     16), so a window's ragged ends cost 256 / P rows, not 256; their keys are the sinks' rows and the window's,
+//     packed into tiles together;
 //   * tree, more than 128 rows: two tiles of rows, every key tile read by both;
 //   * tree, up to 128 rows: the same rows, even key tiles for one stream, odd ones for the other.
 // Prefill writes its rows.  Tree attention splits the key tiles of all units evenly over the CTAs (hata_span.cuh);
@@ -134,8 +135,8 @@ __device__ __forceinline__ void commit_elected(uint64_t* bar) {
 struct Seg {
   int b, g;
   int L, ctx, n_b;
-  int sink_tiles, win_tile;  // list index j -> tile
-  int j0, j1;                // run of the list
+  int sr, base;              // key row r of the run's list is slot r for r < sr, else slot r + base
+  int j0, j1;                // tiles of 128 key rows
   int row0;                  // tree: first row; prefill: first position
   int head0;                 // prefill: first query head
   long long slot;            // tree: partial
@@ -214,7 +215,7 @@ struct Walk {
       s.L = pc.seq.L;
       s.ctx = pc.seq.ctx;
       s.n_b = pc.seq.n_b;
-      s.sink_tiles = s.win_tile = 0;
+      s.sr = s.base = 0;
       s.j0 = pc.j0;
       s.j1 = pc.j1;
       s.row0 = pc.in_seq / p.s.Hkv * (p.pair ? 2 * kTcTile : kTcTile);
@@ -237,11 +238,14 @@ struct Walk {
         s.L = s.ctx = L;
         s.n_b = 0;
         const int t_hi = min(s.row0 + p.pos_block, L) - 1;
-        const int first = max(0, s.row0 - min(p.s.window, s.row0 + 1) + 1) / kTcTile, last = t_hi / kTcTile;
-        s.sink_tiles = min((min(p.s.sink, t_hi + 1) + kTcTile - 1) / kTcTile, first);
-        s.win_tile = first;
+        // The sinks' rows (to a multiple of 8), then the rows from the first one that the block's window
+        // reaches, packed into tiles without the gap between them.
+        const int w0 = max(0, s.row0 - min(p.s.window, s.row0 + 1) + 1), sinks = (min(p.s.sink, t_hi + 1) + 7) / 8 * 8;
+        const bool gap = w0 > sinks;
+        s.sr = gap ? sinks : 0;
+        s.base = gap ? w0 - sinks : 0;
         s.j0 = 0;
-        s.j1 = s.sink_tiles + last - first + 1;
+        s.j1 = (t_hi - s.base) / kTcTile + 1;
         s.slot = 0;
         at += per;
         return true;
@@ -250,10 +254,6 @@ struct Walk {
     }
   }
 };
-
-__device__ __forceinline__ int tile_of(const Seg& s, int j) {
-  return j < s.sink_tiles ? j : s.win_tile + j - s.sink_tiles;
-}
 
 // Visibility words of new tokens, 128 bits in four registers; bit j: token j is seen.
 struct Bits128 {
@@ -271,7 +271,8 @@ struct Bits128 {
 template <bool TREE, bool PAGED>
 __global__ void __maxnreg__(kTcRegs)
     span_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                   const __grid_constant__ CUtensorMap vmap, const TcParams p) {
+                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap kmap8,
+                   const __grid_constant__ CUtensorMap vmap8, const TcParams p) {
   constexpr uint32_t kStages = TREE ? kTcStages : kTcStages - 1;
   extern __shared__ __align__(1024) unsigned char tc_smem[];
   __shared__ __align__(8) uint64_t q_full, q_free, full[kStages], freed[kStages], s_full[2], p_half[2], p_full[2],
@@ -365,7 +366,7 @@ __global__ void __maxnreg__(kTcRegs)
                           &qmap, 64 * (lane & 1), (p.s.Hq * sg.b + head) * p.s.max_seq + pos, &q_full);
         }
       }
-      auto load = [&](const CUtensorMap* map, int tile) -> bool {  // the next ring item
+      auto load = [&](const CUtensorMap* map, const CUtensorMap* map8, int tile) -> bool {  // the next ring item
         const uint32_t st = item % kStages, round = item / kStages;
         if (round > 0 && !wait_warp(&freed[st], (round - 1) & 1)) return false;
         const uint32_t dst = base + kTcRing + st * kTcTileB;
@@ -389,9 +390,16 @@ __global__ void __maxnreg__(kTcRegs)
         } else {
           if (lane == 0) tc::mbar_expect(&full[st], (uint32_t)kTcTileB);
           __syncwarp();
-          if (lane < 2)
-            tc::tma_load_2d(dst + (uint32_t)lane * (kTcTileB / 2), map, 64 * lane,
-                            (p.s.Hkv * sg.b + sg.g) * p.s.max_seq + s0, &full[st]);
+          const int kv = (p.s.Hkv * sg.b + sg.g) * p.s.max_seq;
+          if (s0 >= sg.sr || s0 + kTcTile <= sg.sr) {
+            if (lane < 2)
+              tc::tma_load_2d(dst + (uint32_t)lane * (kTcTileB / 2), map, 64 * lane, kv + s0 + (s0 >= sg.sr ? sg.base : 0),
+                              &full[st]);
+          } else {  // the tile where the sinks end: boxes of 8 rows
+            const int r = (lane >> 1) * 8, row = s0 + r;
+            tc::tma_load_2d(dst + (uint32_t)(lane & 1) * (kTcTileB / 2) + (uint32_t)r * 128u, map8, 64 * (lane & 1),
+                            kv + row + (row >= sg.sr ? sg.base : 0), &full[st]);
+          }
         }
         ++item;
         return true;
@@ -399,8 +407,8 @@ __global__ void __maxnreg__(kTcRegs)
       const int n = sg.j1 - sg.j0, steps = steps_of(n);
       for (int i = 0; ok && i < steps; ++i) {
         const int m = streams_in(n, i);
-        for (int w = 0; ok && w < m; ++w) ok = load(&kmap, tile_of(sg, sg.j0 + (pair ? i : 2 * i + w)));
-        for (int w = 0; ok && w < m; ++w) ok = load(&vmap, tile_of(sg, sg.j0 + (pair ? i : 2 * i + w)));
+        for (int w = 0; ok && w < m; ++w) ok = load(&kmap, &kmap8, sg.j0 + (pair ? i : 2 * i + w));
+        for (int w = 0; ok && w < m; ++w) ok = load(&vmap, &vmap8, sg.j0 + (pair ? i : 2 * i + w));
       }
     }
     // every copy still in flight lands before the CTA leaves
@@ -542,7 +550,8 @@ __global__ void __maxnreg__(kTcRegs)
       }
       float m_used = -INFINITY, l = 0.f;
       for (int i = 0; i < mine; ++i) {
-        const int tile = tile_of(sg, sg.j0 + (pair ? i : 2 * i + w)), s0 = tile * kTcTile;
+        // first key row of the tile, and the slot of that row but for the sinks'
+        const int r0 = (sg.j0 + (pair ? i : 2 * i + w)) * kTcTile, s0 = r0 + sg.base;
         if (!(ok = wait_warp(&s_full[w], tiles & 1))) break;
         ++tiles;
         tc::fence_after();
@@ -558,7 +567,8 @@ __global__ void __maxnreg__(kTcRegs)
         if constexpr (TREE) {
           edge = s0 + kTcTile > sg.ctx;
         } else {
-          edge = s0 + kTcTile > t_lo + 1 || (s0 <= t_hi - p.s.window && s0 + kTcTile > p.s.sink);
+          edge = r0 < sg.sr ? r0 + kTcTile > p.s.sink
+                            : s0 + kTcTile > t_lo + 1 || (s0 <= t_hi - p.s.window && s0 + kTcTile > p.s.sink);
         }
         if (edge) {
 #pragma unroll
@@ -570,6 +580,8 @@ __global__ void __maxnreg__(kTcRegs)
               const int e0 = s0 + 32 * k;
               v = span::low_bits(t + 1 - e0) &
                   (~span::low_bits(t - min(p.s.window, t + 1) + 1 - e0) | span::low_bits(min(p.s.sink, sg.L) - e0));
+              const int r = r0 + 32 * k;
+              if (r < sg.sr) v = (v & ~span::low_bits(sg.sr - r)) | span::low_bits(min(p.s.sink, sg.sr) - r);
             }
             if (!__any_sync(0xffffffffu, v != 0u)) none |= 1u << k;
             if (__any_sync(0xffffffffu, v != 0xffffffffu)) {
@@ -716,7 +728,17 @@ __global__ void __maxnreg__(kTcRegs)
         // & 7)), then eight lanes per row, so a store covers four rows of 128 bytes instead of 32 of 16.
         const float inv = l == 0.f ? 0.f : 1.f / l;
         unsigned char* stage = tc_smem + (base - tc::smem_u32(tc_smem)) + kTcOut + (uint32_t)warp * 4096u;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.s.out);
+        // 16 rows that begin at a multiple of 16 are one head's: this lane's row and piece of the first and second 16
+        int pos[2];
+        __nv_bfloat16* out[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int mr = (warp & 3) * 32 + 16 * k + (lane >> 3);
+          const int head = sg.head0 + (p.prefill_heads == 1 ? 0 : w * (p.prefill_heads >> 1) + (mr >> p.pos_shift));
+          pos[k] = t_lo + (mr & (p.q_box - 1));
+          out[k] = static_cast<__nv_bfloat16*>(p.s.out) +
+                   ((size_t)(sg.b * p.s.Hq + head) * p.s.max_seq + pos[k]) * kHeadDim + 8 * (lane & 7);
+        }
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           __syncwarp();  // the other half's rows have been read
@@ -739,12 +761,8 @@ __global__ void __maxnreg__(kTcRegs)
           for (int e = 0; e < 8; ++e) {
             const int r = 4 * e + (lane >> 3), q = lane & 7;  // row of the warp, piece
             const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((q ^ (r & 7)) << 4));
-            const int mr = (warp & 3) * 32 + r;  // row of the stream
-            const int head = sg.head0 + (p.prefill_heads == 1 ? 0 : w * (p.prefill_heads >> 1) + (mr >> p.pos_shift));
-            const int tr = t_lo + (mr & (p.q_box - 1));
-            if (tr < sg.L)
-              *reinterpret_cast<uint4*>(out + ((size_t)(sg.b * p.s.Hq + head) * p.s.max_seq + tr) * kHeadDim + 64 * half +
-                                        8 * q) = v;
+            if (pos[e >> 2] + 4 * (e & 3) < sg.L)
+              *reinterpret_cast<uint4*>(out[e >> 2] + 4 * (e & 3) * kHeadDim + 64 * half) = v;
           }
         }
       }
@@ -868,7 +886,7 @@ cudaError_t launch_span_tc(const hata_dims_t& d, const span::Params& s, const Pa
   cudaError_t e = pg ? configure_tc<true, true>() : configure_tc<true, false>();
   if (e != cudaSuccess) return e;
   e = launch_early(pg ? span_tc_kernel<true, true> : span_tc_kernel<true, false>, dim3((unsigned)sms), kTcThreads, kTcSmem, st,
-                   qm, km, vm, p);
+                   qm, km, vm, km, vm, p);
   if (e != cudaSuccess) return e;
   return launch_early(span_merge_kernel, dim3((unsigned)units, kHeadDim / 4, p.pair ? 2 : 1), kTcTile, 0, st, p, sms, rows);
 }
@@ -901,16 +919,17 @@ cudaError_t launch_window_prefill(const hata_dims_t& d, const void* q, const voi
   p.box_rows = kTcTile;
   const long long q_rows = (long long)d.batch * d.n_q_heads * d.max_seq, kv_rows = (long long)d.batch * d.n_kv_heads * d.max_seq;
   if (q_rows + 2 * kTcTile > 0x7fffffffLL) return cudaErrorNotSupported;
-  CUtensorMap qm, km, vm;
+  CUtensorMap qm, km, vm, km8, vm8;
   if (!make_bf16_rows_map(&qm, q, q_rows, p.q_box) || !make_bf16_rows_map(&km, K, kv_rows, kTcTile) ||
-      !make_bf16_rows_map(&vm, V, kv_rows, kTcTile))
+      !make_bf16_rows_map(&vm, V, kv_rows, kTcTile) || !make_bf16_rows_map(&km8, K, kv_rows, 8) ||
+      !make_bf16_rows_map(&vm8, V, kv_rows, 8))
     return cudaErrorNotSupported;
   cudaError_t e = configure_tc<false, false>();
   if (e != cudaSuccess) return e;
   const long long items = (long long)p.n_blocks_pos * p.rows_of_items;
   if (items > 0x3fffffffLL) return cudaErrorNotSupported;
   const unsigned grid = (unsigned)std::min<long long>(items, span_sms());
-  return launch_early(span_tc_kernel<false, false>, dim3(grid), kTcThreads, kTcSmem, st, qm, km, vm, p);
+  return launch_early(span_tc_kernel<false, false>, dim3(grid), kTcThreads, kTcSmem, st, qm, km, vm, km8, vm8, p);
 }
 
 }  // namespace hata

@@ -50,7 +50,7 @@ def test_lengths(H, L):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("window,sink", [(1, 0), (1, 5), (2, 128), (127, 0), (128, 1), (129, 129), (333, 130), (10**9, 0),
-                                         (5, 10**9), (700, 700), (2**31 - 1, 2**31 - 1)])
+                                         (5, 10**9), (700, 700), (100, 300), (64, 9), (70, 136), (200, 640), (2**31 - 1, 2**31 - 1)])
 def test_windows(H, window, sink):
     case(H, 4, 2, 1025, [1025, 0, 700, 1], window, sink, seed=window % 997 + sink % 997)
 
