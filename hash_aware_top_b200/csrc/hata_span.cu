@@ -7,9 +7,9 @@
 // into P in place (the accumulator of S has the layout of the A operand of P.V), and adds P.V to its own running
 // output.  No barrier inside a run of tiles.  The warps meet once per unit.  Bound by memory: at 6.5 TB/s an SM
 // receives a warp's 8 KB step every 364 cycles, and 128 KB are in flight.  Measured on B200: 16 ragged sequences of
-// 8207 visible slots, 32 / 8 heads, paged, 89-92 us (0.89-0.93 of a copy's bandwidth); 8 x 64K slots 329 us (1.00); 28 rows over
+// 8207 visible slots, 32 / 8 heads, paged, 87-91 us (0.91-0.94 of a copy's bandwidth); 8 x 64K slots 329 us (1.00); 28 rows over
 // 29K slots 31 us (0.58: 3 us of launches, 2 us to find the run, 2 us to meet and 2 us to join are fixed costs); 4 rows
-// over 4.1K slots 10 us.
+// over 4.1K slots 9.3 us.
 //
 // span_simt_kernel (fp32): eight warps, each with 16 slots of a 128-slot tile, on its own: it copies
 // its rows of K and V to shared memory (cp.async), a lane takes one slot and half of the 128 dimensions for the
