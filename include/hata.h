@@ -410,7 +410,8 @@ HATA_API hata_status_t hata_window_decode_paged(const hata_dims_t* dims, const v
  * iff s <= t and (s < n_sink or s > t - window):
  *     out[b][h][t] = sum_s softmax_s(scale * q[b][h][t] . K[b][g][s]) V[b][g][s]
  * Layouts, types (bf16) and rounding of hata_prefill_attention; rows t >= L_b of out are
- * not written, and rows of K and V at or past L_b may hold anything.  window >= 1,
+ * not written, and rows of K and V at or past L_b may hold anything; rows before it must
+ * be finite (one that is not may reach rows of out that do not see it).  window >= 1,
  * n_sink >= 0; scale <= 0 selects 1/sqrt(d).  L_b > max_seq is clamped and flagged; a
  * bounded wait that runs out records HATA_ERR_TIMEOUT.  The workspace is at least
  * 16 bytes: its status word.  (The keys' codes: hata_encode_append.)
@@ -431,7 +432,8 @@ HATA_API hata_status_t hata_window_prefill(const hata_dims_t* dims, const void* 
  *            for token j; bits of tokens j >= n_b are ignored
  *   n_tok    1 .. 128
  * A token that sees nothing gives zeros.  Slots that no token sees may hold anything;
- * a value row that some token sees must be finite.  A sequence with n_b outside
+ * a value row that some token sees must be finite (one that is not may reach tokens that do
+ * not see it).  A sequence with n_b outside
  * [0, n_tok] or L_b outside [n_b, max_seq] is flagged and its rows left as they were.
  * scale, types, paging and rounding as in hata_window_decode.
  */
