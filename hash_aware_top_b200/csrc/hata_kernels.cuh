@@ -53,6 +53,9 @@ cudaError_t launch_append_kv(const hata_dims_t& d, const void* new_k, const void
 
 // Launches a kernel that may be set up while the one before it on the stream still runs: the kernel waits for that
 // one to end (griddepcontrol.wait) before it reads what that one may have written, and before it writes anything.
+// A kernel that comes next waits for this grid alone, so this grid must not end before the ones ahead of it have: at
+// least one CTA waits whatever the inputs are, and a thread that returns without waiting has touched nothing that those
+// kernels touch but their common inputs.
 template <typename... Params, typename... Args>
 cudaError_t launch_early(void (*k)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
                          const Args&... args) {

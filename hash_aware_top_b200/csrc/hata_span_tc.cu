@@ -789,17 +789,16 @@ __global__ void __maxnreg__(kMergeRegs) span_merge_kernel(const TcParams p, int 
   const int upt = p.s.Hkv * p.s.row_tiles, unit = (int)blockIdx.x, b = unit / upt, in_seq = unit % upt;
   // the lengths are the call's inputs: where the partials lie is found while the main kernel still runs
   const span::Seq sq = span::seq_of(p.s, b);
-  if (sq.tiles == 0) return;
-  const span::Runs runs = span::runs_of(p.s, lane, grid_tc, b, in_seq, sq);
+  const span::Runs runs = sq.tiles > 0 ? span::runs_of(p.s, lane, grid_tc, b, in_seq, sq) : span::Runs{};
   const int g = in_seq % p.s.Hkv, half = blockIdx.z;  // half: of a pair, the row tile
   const int m = threadIdx.x, q4 = (int)blockIdx.y;
   const int row = in_seq / p.s.Hkv * rows_per_unit + half * kTcTile + m;
-  if (row >= p.s.R || row % p.s.T >= sq.n_b) return;
   // a row's partials: one per run and, if its key tiles were shared out over both streams, stream
   const int n_str = p.pair ? 1 : 2, n = runs.n * n_str;
   const float* first = p.s.part + ((size_t)(unit + runs.cta0) * 2 + (p.pair ? half : 0)) * kPartFloats + m;
   const size_t step = (size_t)kPartFloats * (p.pair ? 2 : 1);
-  ptx::pdl_wait();
+  ptx::pdl_wait();  // also where there is nothing to join: what comes next on the stream waits for this grid alone
+  if (sq.tiles == 0 || row >= p.s.R || row % p.s.T >= sq.n_b) return;
   float M = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = 0; i0 < n; i0 += kMergeBatch) {
