@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kRopeCtas) norm_rope_kernel(c
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           const float other = INTER ? x[k ^ 1] : __shfl_sync(0xffffffffu, x[k], partner);
-          y[k] = rs * fmaf(x[k], fa[k], other * fb[k]);
+          y[k] = rs * (turns ? fmaf(x[k], fa[k], other * fb[k]) : x[k] * fa[k]);  // not turned: no 0 * infinity
         }
         const int r = r0 + u * RPS + sub;
         if (r < hi && write) *reinterpret_cast<uint4*>(d0 + (size_t)r * dst_stride * kHeadDim) = Vec16<T>::pack(y);

@@ -131,6 +131,38 @@ def test_no_norm(H):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("rot", [0, 32, 96])
+def test_elements_that_do_not_turn_are_copies_without_a_weight(H, dtype, inter, rot):
+    """Infinities, NaN, zeros of both signs and their neighbours: y = x for every element past rot_dim, bit for bit."""
+    B, T, Hq, Hkv, L = 1, 2, 3, 1, 8
+    d = H.dims_for(B, Hq, Hkv, D, 128, L, dtype)
+    g = torch.Generator(device="cuda").manual_seed(rot)
+    x = torch.randn(B, T, Hq + 2 * Hkv, D, generator=g, device="cuda").to(dtype)
+    x[..., 100], x[..., 103], x[..., 106], x[..., 127] = float("inf"), float("-inf"), float("nan"), -0.0
+    q_out = torch.zeros(B, Hq, T, D, device="cuda", dtype=dtype)
+    K, V = torch.zeros(2, B, Hkv, L, D, device="cuda", dtype=dtype).unbind(0)
+    lens, ws = torch.tensor([5], dtype=torch.int32, device="cuda"), torch.zeros(16, dtype=torch.uint8, device="cuda")
+    table = H.hata_rope_table(L, rot, 1e4) if rot else None
+    H.hata_norm_rope(d, x[:, :, :Hq], x[:, :, Hq:Hq + 1], x[:, :, Hq + 1:], None, None, EPS, table, inter, None, None, lens,
+                     q_out, K, V, ws)
+    assert H.hata_read_device_status(ws) == 0
+    bits = lambda t: t.contiguous().view(torch.int32 if dtype == torch.float32 else torch.int16)  # noqa: E731
+    nan = torch.isnan(x)
+    for got, want, n in ((q_out[0].transpose(0, 1), x[0, :, :Hq], nan[0, :, :Hq]),
+                         (K[0, :, 3:5].transpose(0, 1), x[0, :, Hq:Hq + 1], nan[0, :, Hq:Hq + 1])):
+        assert torch.equal(torch.isnan(got), n)
+        assert torch.equal(bits(got[..., rot:])[~n[..., rot:]], bits(want[..., rot:])[~n[..., rot:]])
+    # with a weight, elements that do not turn are x r w of their own x alone
+    x[..., 100], x[..., 103], x[..., 106] = 1e18, -1e18, 0.0
+    w = torch.ones(D, device="cuda")
+    w[102] = float("inf")  # the weight of an interleaved neighbour
+    H.hata_norm_rope(d, x[:, :, :Hq], x[:, :, Hq:Hq + 1], x[:, :, Hq + 1:], w, w, EPS, table, inter, None, None, lens, q_out, K, V, ws)
+    assert bool(torch.isfinite(q_out[..., 103]).all()) and bool(torch.isfinite(K[0, :, 3:5, 103]).all())
+
+
+@pytest.mark.gpu
 def test_table(H):
     """Angles in 64 bits, rounded once: half a step of fp32 of values up to 1, and as much again for the 64-bit
     functions' last places at far positions (t = 2e5 has angles of 2e5 * 2^-53)."""
