@@ -14,6 +14,12 @@ bool ok16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool ok4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool null_or4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// Whether two int32 arrays share memory (a null array: no).
+bool overlap(const int32_t* a, size_t n_a, const int32_t* b, size_t n_b) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a && b && a0 < b0 + 4 * n_b && b0 < a0 + 4 * n_a;
+}
+
 hata_status_t status_of(cudaError_t e) {
   if (e == cudaSuccess) return HATA_OK;
   return e == cudaErrorNotSupported ? HATA_ERR_UNSUPPORTED : HATA_ERR_CUDA;
@@ -224,6 +230,11 @@ static hata_status_t compact(const hata_dims_t* dims, int n_tok, const int32_t* 
     return HATA_ERR_INVALID_ARG;
   if (n_tok < 1 || n_tok > dims->max_seq) return HATA_ERR_INVALID_ARG;
   if (!ok16(ws) || ws_bytes < kStatusBytes) return HATA_ERR_WORKSPACE;
+  // new_lens is written while other CTAs of the sequence may still read the call's int32 inputs
+  const size_t B = (size_t)dims->batch;
+  if (overlap(new_lens, B, keep, B * (size_t)n_tok) || overlap(new_lens, B, n_keep, B) || overlap(new_lens, B, n_new, B) ||
+      overlap(new_lens, B, seq_lens, B) || (pg && overlap(new_lens, B, pg->block_table, B * (size_t)pg->max_blocks)))
+    return HATA_ERR_INVALID_ARG;
   return status_of(launch_compact(*dims, n_tok, keep, n_keep, n_new, seq_lens, K, V, codes, pg, new_lens,
                                   static_cast<uint32_t*>(ws), static_cast<cudaStream_t>(stream)));
 }

@@ -481,7 +481,8 @@ HATA_API hata_status_t hata_pages_resize(const hata_dims_t* dims, const int32_t*
  * Accepted rows moved to the front of the newest n_b tokens (after a tree attention, or
  * to drop any of the newest tokens): with base = seq_lens[b] - n_b, for j < n_keep[b]
  * rows base + keep[b][j] of K, V and, if not NULL, codes go to base + j, and
- * new_lens[b] = base + n_keep[b] (new_lens may be NULL and must not be seq_lens).
+ * new_lens[b] = base + n_keep[b] (new_lens may be NULL and must share no memory with the
+ * call's inputs).
  *   keep   device [B][n_tok] int32, its first n_keep[b] strictly ascending in [0, n_b)
  *   n_new  device [B] int32, or NULL for n_tok; n_tok in [1, max_seq]
  * seq_lens is not changed (the paged form's pages are released by hata_pages_resize to

@@ -283,3 +283,23 @@ def test_refusals(H):
     assert comp(lens=null) == 1 and comp(new=P(0x2000)) == 1 and comp(ws=null) == 5 and comp(wsb=8) == 5
     assert H.lib.hata_compact_kv_paged(ctypes.byref(d), 4, f, f, null, P(0x2000), f, f, null, null, 16, 4, f, f, 16, null) == 1
     assert H.hata_status_string(H.HATA_ERR_NO_PAGES) == "too few free pages in the pool"
+
+
+def test_compact_refuses_new_lens_over_its_inputs(H):
+    """new_lens is written while other CTAs still read keep, n_keep, n_new, seq_lens and the table."""
+    P = ctypes.c_void_p
+    f, null, d = P(0x100000), P(0), H.dims_for(5, 4, 2, D, 128, 64, "bf16")
+    at = dict(keep=0x1000, n_keep=0x2000, n_new=0x3000, lens=0x4000, table=0x5000, new=0x6000)  # 80, 20, 20, 20, 80 bytes
+
+    def call(paged, **kw):
+        a = {k: P(v) for k, v in {**at, **kw}.items()}
+        head = (ctypes.byref(d), 4, a["keep"], a["n_keep"], a["n_new"], a["lens"], f, f, f)
+        if paged:
+            return H.lib.hata_compact_kv_paged(*head, a["table"], 16, 4, a["new"], f, 16, null)
+        return H.lib.hata_compact_kv(*head, a["new"], f, 16, null)
+
+    for paged in (False, True):
+        for name, size in (("keep", 80), ("n_keep", 20), ("n_new", 20), ("lens", 20)):
+            for off in (-16, 0, 4, size - 4):
+                assert call(paged, new=at[name] + off) == 1, (paged, name, off)
+    assert call(True, new=at["table"]) == 1 and call(True, new=at["table"] + 76) == 1
