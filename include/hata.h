@@ -356,7 +356,8 @@ HATA_API hata_status_t hata_prefill_attention(const hata_dims_t* dims, const voi
  * A sequence with n_b outside [0, n_tok] or seq_lens[b] outside [n_b, max_seq], a
  * token whose position lies outside [0, n_pos), and the cache rows of a token whose
  * block number lies outside the pool are left unwritten and flagged in the status
- * word.  Inputs and outputs must not overlap.  batch at most 65535.
+ * word.  Inputs and outputs must not overlap.  In the paged form the pages of the new tokens must belong
+ * to one sequence each (after a fork, hata_pages_resize sees to it); this is not checked.  batch at most 65535.
  */
 HATA_API hata_status_t hata_norm_rope(const hata_dims_t* dims, int n_tok, const void* q_in, long long q_stride,
                                       const void* k_in, long long k_stride, const void* v_in, long long v_stride,
@@ -487,8 +488,11 @@ HATA_API hata_status_t hata_pages_resize(const hata_dims_t* dims, const int32_t*
  *   n_new  device [B] int32, or NULL for n_tok; n_tok in [1, max_seq]
  * seq_lens is not changed (the paged form's pages are released by hata_pages_resize to
  * new_lens).  A sequence whose keep or lengths break these rules is flagged and left as it is
- * (new_lens[b] = seq_lens[b]); rows in blocks outside the pool are flagged and skipped.  The workspace
- * is at least 16 bytes: its status word.  batch at most 65535.
+ * (new_lens[b] = seq_lens[b]); rows in blocks outside the pool are flagged and skipped.  In the paged form so is
+ * a sequence with a row to move onto a slot that another sequence holds too: one below the other's length,
+ * in a page that the block table names for both in the same column, as after hata_pages_fork until
+ * hata_pages_resize grows them.  (Pages shared in different columns are not looked for and must not be
+ * compacted.)  The workspace is at least 16 bytes: its status word.  batch at most 65535.
  */
 HATA_API hata_status_t hata_compact_kv(const hata_dims_t* dims, int n_tok, const int32_t* keep, const int32_t* n_keep,
                                        const int32_t* n_new, const int32_t* seq_lens, void* K, void* V, void* codes,

@@ -303,3 +303,120 @@ def test_compact_refuses_new_lens_over_its_inputs(H):
             for off in (-16, 0, 4, size - 4):
                 assert call(paged, new=at[name] + off) == 1, (paged, name, off)
     assert call(True, new=at["table"]) == 1 and call(True, new=at["table"] + 76) == 1
+
+
+def pad(rows, T):
+    return torch.tensor([r + [0] * (T - len(r)) for r in rows], dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,r", [(torch.bfloat16, 128), (torch.float32, 16)])
+def test_compact_leaves_rows_that_another_sequence_holds(H, dtype, r):
+    """After a fork the drafted rows lie in pages of several sequences: a sequence that would move some of them is flagged
+    and left; one that moves nothing, or only rows past the other's end, is not."""
+    B, T, bs = 5, 6, 16
+    c = Cache(H, B, 40, bs, 100, r=r, dtype=dtype)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    ws = torch.zeros(16, dtype=torch.uint8, device="cuda")
+    new_lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+
+    def compact(keep, n_new):
+        c.H.hata_compact_kv_paged(c.d, pad(keep, T), i32([len(k) for k in keep]), i32(n_new), c.lens, c.K, c.V, c.codes, c.table, bs,
+                                  new_lens, ws)
+        return c.H.hata_read_device_status(ws)
+
+    def rows(t, b, n):
+        at = torch.arange(n, device="cuda")
+        return t[c.table[b].long()[at // bs], :, at % bs]
+
+    def held(lens):
+        return [[rows(t, b, n).clone() for b, n in enumerate(lens)] for t in c.tensors()]
+
+    c.resize([0, 45, 38, 30, 0])
+    c.fork([1, 1, 2, 3, 3])  # 0 and 1 share pages, 3 and 4 do
+    assert c.lens.tolist() == [45, 45, 38, 30, 30] and c.status() == 0
+    before = held(c.lens.tolist())
+    # 0 and 1 keep other paths of shared rows, 2 is alone, 3 moves nothing, 4 keeps nothing
+    assert compact([[0, 2, 5], [1, 3], [1, 4, 5], [0, 1, 2], []], [6, 6, 6, 6, 6]) == H.HATA_ERR_INVALID_ARG
+    assert new_lens.tolist() == [45, 45, 35, 27, 24]
+    for old, t in zip(before, c.tensors()):
+        for b in (0, 1, 3, 4):
+            assert torch.equal(rows(t, b, len(old[b])), old[b])
+        assert torch.equal(rows(t, 2, 35), torch.cat([old[2][:32], old[2][[33, 36, 37]]]))
+    # the other holds the page, but not the rows that move: 4 goes back to 25 rows, 3 keeps rows 25 to 29 in other places
+    c.resize([45, 45, 35, 30, 25])
+    before = held([45, 45, 35, 30, 25])
+    assert compact([[], [], [], [1, 3], []], [0, 0, 0, 5, 0]) == 0 and new_lens.tolist() == [45, 45, 35, 27, 25]
+    for old, t in zip(before, c.tensors()):
+        assert torch.equal(rows(t, 3, 27), torch.cat([old[3][:25], old[3][[26, 28]]]))
+        assert torch.equal(rows(t, 4, 25), old[4][:25])
+    # a first moved row below the other's end is one too many
+    assert compact([[], [], [], [1, 3], []], [0, 0, 0, 6, 0]) == H.HATA_ERR_INVALID_ARG and new_lens.tolist()[3] == 30
+    # and entries past a sequence's end hold nothing
+    c.resize([45, 0, 35, 30, 0])
+    c.table[1] = c.table[0]
+    c.table[4] = c.table[3]
+    assert compact([[2], [], [], [5], []], [6, 0, 0, 6, 0]) == 0 and new_lens.tolist() == [40, 0, 35, 25, 0]
+
+
+@pytest.mark.gpu
+def test_beams_that_fork_then_grow_keep_their_own_paths(H):
+    """Fork first, then grow: every beam's drafted rows are its own, and each keeps another path."""
+    B, T, bs, L = 4, 5, 16, 27
+    c = Cache(H, B, 30, bs, 64)
+    c.resize([L, 0, 0, 0])
+    c.fork([0, 0, 0, 0])
+    c.resize([L + T] * B)
+    at = torch.arange(L + T, device="cuda")
+    place = [(c.table[b].long()[at // bs], at % bs) for b in range(B)]
+    for t in c.tensors():  # the drafted rows of each beam
+        for b in range(B):
+            page, off = place[b][0][L:], place[b][1][L:]
+            t[page, :, off] = (torch.arange(b * T, (b + 1) * T, device="cuda")[:, None, None]).expand(T, t.shape[1], t.shape[3]).to(t.dtype)
+    want = [[t[p, :, o].clone() for p, o in place] for t in c.tensors()]
+    keep = [[0, 2], [1, 2, 4], [4], [0, 1, 2, 3, 4]]
+    new_lens, ws = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(16, dtype=torch.uint8, device="cuda")
+    H.hata_compact_kv_paged(c.d, pad(keep, T), torch.tensor([len(k) for k in keep], dtype=torch.int32, device="cuda"), None, c.lens,
+                            c.K, c.V, c.codes, c.table, bs, new_lens, ws)
+    assert H.hata_read_device_status(ws) == 0 and new_lens.tolist() == [L + len(k) for k in keep]
+    for t, w in zip(c.tensors(), want):
+        for b, (p, o) in enumerate(place):
+            n = L + len(keep[b])
+            assert torch.equal(t[p[:n], :, o[:n]], torch.cat([w[b][:L], w[b][L:][keep[b]]]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("B,Hkv,r,dtype", [(300, 3, 16, torch.bfloat16), (210, 2, 64, torch.float32), (260, 5, 256, torch.bfloat16)])
+def test_compact_of_many_sequences(H, paged, B, Hkv, r, dtype):
+    """So many that a CTA takes several heads, odd numbers of heads among them."""
+    T, max_seq, bs = 40, 64, 16
+    g = torch.Generator().manual_seed(B)
+    d = H.dims_for(B, Hkv, Hkv, D, r, max_seq, dtype)
+    nb = max_seq // bs
+    lead = (B * nb, Hkv, bs) if paged else (B, Hkv, max_seq)
+    bt = torch.randperm(B * nb, generator=g).int().view(B, nb).cuda()
+    tensors = [torch.randn(*lead, D, device="cuda").to(dtype), torch.randn(*lead, D, device="cuda").to(dtype),
+               torch.randint(-2**15, 2**15, d.code_shape(*lead), device="cuda", dtype=torch.int32 if r != 16 else torch.int16)]
+    lens = torch.randint(T, max_seq + 1, (B,), generator=g)
+    n_keep = torch.randint(0, T + 1, (B,), generator=g)
+    keep = torch.stack([torch.cat([torch.randperm(T, generator=g)[:n].sort()[0], torch.full((T - n,), -1)]) for n in n_keep.tolist()])
+    b = torch.arange(B)[:, None].expand(B, T)
+    j = torch.arange(T)[None].expand(B, T)
+    ok = j < n_keep[:, None]
+    b, src, dst = b[ok].cuda(), ((lens - T)[:, None] + keep)[ok].cuda(), ((lens - T)[:, None] + j)[ok].cuda()
+    want = [t.clone() for t in tensors]
+    for t, w in zip(tensors, want):
+        if paged:
+            w[bt[b, dst // bs].long(), :, dst % bs] = t[bt[b, src // bs].long(), :, src % bs]
+        else:
+            w[b, :, dst] = t[b, :, src]
+    new_lens, ws = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(16, dtype=torch.uint8, device="cuda")
+    args = (d, keep.int().cuda(), n_keep.int().cuda(), None, lens.int().cuda(), *tensors)
+    if paged:
+        H.hata_compact_kv_paged(*args, bt, bs, new_lens, ws)
+    else:
+        H.hata_compact_kv(*args, new_lens, ws)
+    assert H.hata_read_device_status(ws) == 0 and new_lens.tolist() == (lens - T + n_keep).tolist()
+    for got, w in zip(tensors, want):
+        assert torch.equal(got, w)
