@@ -86,7 +86,7 @@ typedef enum { HATA_F32 = 0, HATA_BF16 = 1 } hata_dtype_t;
 /* Problem shape, shared by every call. */
 typedef struct {
   int batch;      /* B >= 1 */
-  int n_q_heads;  /* Hq >= 1, a multiple of n_kv_heads */
+  int n_q_heads;  /* Hq >= 1, G * n_kv_heads with G <= 16 (else HATA_ERR_UNSUPPORTED) */
   int n_kv_heads; /* Hkv >= 1 */
   int head_dim;   /* d; this version supports 128 */
   int hash_bits;  /* r in {16, 32, 64, 128, 256}; 16 needs an even max_seq */
@@ -391,7 +391,7 @@ HATA_API hata_status_t hata_span_workspace_size(const hata_dims_t* dims, int n_t
  * for layers that keep no top-k: with L_b = seq_lens[b], query head h in group g sees slot s
  * iff s < L_b and (s < n_sink or s >= L_b - window):
  *     out[b][h] = sum_s softmax_s(scale * q[b][h] . K[b][g][s]) V[b][g][s]
- * Layouts of hata_dense_decode; fp32 or bf16, any G.  window >= 1, n_sink >= 0; scale
+ * Layouts of hata_dense_decode; fp32 or bf16, G = 1 .. 16.  window >= 1, n_sink >= 0; scale
  * <= 0 selects 1/sqrt(d).  An empty sequence (L_b <= 0) gives zeros; L_b > max_seq is
  * clamped and flagged.  Slots that are not visible may hold anything.  In the paged form a
  * block number outside the pool is replaced by block 0 and flagged.  bf16 probabilities

@@ -388,3 +388,20 @@ def test_refusals(H):
     assert tree(wsb=64) == 5 and tree(ws=null) == 5
     assert H.lib.hata_tree_attention_paged(ctypes.byref(d), 4, f, f, f, f, 12, 4, f, null, null, 0.0, f, f, 1 << 40, null) == 1
     assert H.lib.hata_window_decode_paged(ctypes.byref(d), f, f, f, null, 16, 4, f, 4, 0, 0.0, f, f, 1 << 40, null) == 1
+
+
+def test_group_sizes(H):
+    """Up to 16 query heads for a KV head, in every call; more are unsupported."""
+    P = ctypes.c_void_p
+    f, null, n = P(0x1000), P(0), ctypes.c_size_t(0)
+    for G, status in ((16, 0), (17, 2), (32, 2)):
+        d = ctypes.byref(H.dims_for(1, 2 * G, 2, D, 128, 64, "bf16"))
+        assert H.lib.hata_span_workspace_size(d, 4, ctypes.byref(n)) == status
+        assert H.lib.hata_pages_workspace_size(d, ctypes.byref(n)) == status
+        # a bad argument where the group is allowed, so that nothing is launched
+        assert H.lib.hata_window_decode(d, null, f, f, f, 4, 0, 0.0, f, f, 1 << 40, null) == (status or 1)
+        assert H.lib.hata_window_prefill(d, null, f, f, f, 4, 0, 0.0, f, f, 16, null) == (status or 1)
+        assert H.lib.hata_tree_attention(d, 4, null, f, f, f, null, null, 0.0, f, f, 1 << 40, null) == (status or 1)
+        assert H.lib.hata_norm_rope(d, 1, null, 4096, f, 256, f, 256, null, null, 1e-6, f, 64, 128, 0, null, null, f, f, f, f, f, 16,
+                                    null) == (status or 1)
+        assert H.lib.hata_compact_kv(d, 4, null, f, null, f, f, f, null, null, f, 16, null) == (status or 1)
