@@ -8,7 +8,8 @@ CUDA stream to the library.  All computation happens in the CUDA kernels of
 libhata.so; there is no CPU fallback, and importing this package fails loudly
 when the library has not been built (python hash_aware_top_b200/build.py).
 Most calls go through ctypes; those of the serving operators through a native
-module (_serving) with the same checks.
+module (_serving) with the same checks, which is tied to the torch it was built
+for.  Where it is missing or was built for another, those calls alone fail.
 
 Function names and argument order follow include/hata.h.
 """
@@ -201,7 +202,28 @@ def _load():
 
 lib = _load()
 
-from . import _serving  # noqa: E402  (native; needs libhata.so, which is loaded now)
+class _Unbuilt:
+    """In place of the native half of the binding where that cannot be used: the calls that need it fail, and say why."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"the native half of the binding {self._why}; build it with: python hash_aware_top_b200/build.py")
+
+
+def _load_serving():
+    from .build import binding_built_for
+
+    try:
+        from . import _serving  # needs libhata.so, which is loaded now
+    except ImportError as e:
+        return _Unbuilt(f"cannot be loaded ({e})")
+    have, here = getattr(_serving, "built_for", "an unknown torch"), binding_built_for()
+    return _serving if have == here else _Unbuilt(f"was built for {have}, not {here}")
+
+
+_serving = _load_serving()
 
 
 def hata_status_string(status: int) -> str:

@@ -391,4 +391,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__serving() { return PyModule_Create(&module); }
+// built_for: the torch and the interpreter whose headers this was compiled with; the package compares it with those it runs on.
+PyMODINIT_FUNC PyInit__serving() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", HATA_BUILT_FOR) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -7,14 +7,16 @@
 Compiles every hash_aware_top_b200/csrc/*.cu to an object under _build/ and
 links them into hash_aware_top_b200/libhata.so (CUDA runtime linked
 statically), then the benchmark's loop (libhata_e2e.so) and the native half of
-the binding (_serving.so, g++ against the headers of the installed torch).
-Rebuilds only when a source or header is newer than the library.
+the binding (_serving.<ABI>.so, g++ against the headers of the installed torch).
+Rebuilds only when a source or header is newer than the library; the native
+half also when torch, the interpreter or the compiler's command is another.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import glob
+import json
 import os
 import shutil
 import subprocess
@@ -112,29 +114,50 @@ def build_e2e(cc, flags, verbose=False):
 
 
 BINDING_SRC = os.path.join(PKG, "binding", "serving.cpp")
-BINDING_LIB = os.path.join(PKG, "_serving.so")
+BINDING_LIB = os.path.join(PKG, "_serving" + sysconfig.get_config_var("EXT_SUFFIX"))  # an interpreter finds its own alone
+BINDING_STAMP = os.path.join(BUILD, "serving.json")
+
+
+def binding_built_for() -> str:
+    """What the native half of the binding is tied to; it is compiled in and compared when the package is imported."""
+    import torch
+
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
 
 
 def build_binding(force=False, verbose=False):
-    """The native half of the Python binding.  It calls the C ABI, so it is rebuilt when a header changes."""
-    if not force and not _stale(BINDING_LIB, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))):
-        return
+    """The native half of the Python binding.  It calls the C ABI and torch's, so it is rebuilt when a header changes and
+    when the command does: another torch, interpreter or compiler."""
     import torch  # its headers, its ABI
 
     base = os.path.dirname(torch.__file__)
     tmp = BINDING_LIB + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DHATA_BUILT_FOR="{binding_built_for()}"', "-I", INCLUDE,
            "-I", os.path.join(base, "include"), "-I", sysconfig.get_paths()["include"],
            "-I", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
            BINDING_SRC, "-o", tmp, "-L" + PKG, "-lhata", "-L" + os.path.join(base, "lib"), "-ltorch_python",
            "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    try:
+        with open(BINDING_STAMP) as f:
+            same = json.load(f) == cmd
+    except (OSError, ValueError):
+        same = False
+    if not force and same and not _stale(BINDING_LIB, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+        return
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"binding build failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING_LIB)
+    os.makedirs(os.path.dirname(BINDING_STAMP), exist_ok=True)
+    with open(BINDING_STAMP, "w") as f:
+        json.dump(cmd, f)
+    untagged = os.path.join(PKG, "_serving.so")  # as builds made it before, for any interpreter to find
+    if os.path.exists(untagged):
+        os.remove(untagged)
 
 
 def main(argv=None):
