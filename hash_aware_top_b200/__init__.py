@@ -549,7 +549,8 @@ def hata_norm_rope(dims: Dims, q_in, k_in, v_in, q_weight, k_weight, eps, table,
 
 def hata_norm_rope_paged(dims: Dims, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions,
                          seq_lens, q_out, K_pool, V_pool, block_table, block_size, ws, stream=None):
-    """hata_norm_rope into paged pools ([n_blocks][Hkv][block_size][d])."""
+    """hata_norm_rope into paged pools ([n_blocks][Hkv][block_size][d]).  The new tokens' pages must be their sequence's own:
+    hata_pages_resize sees to it after a fork."""
     _check(_serving.norm_rope(dims, q_in, k_in, v_in, q_weight, k_weight, eps, table, interleaved, n_new, positions, seq_lens,
                               q_out, K_pool, V_pool, block_table, block_size, ws, _handle(stream), True),
            "hata_norm_rope_paged")
@@ -617,14 +618,15 @@ def hata_pages_resize(dims: Dims, new_lens, K_pool, V_pool, codes_pool, block_ta
 
 def hata_compact_kv(dims: Dims, keep, n_keep, n_new, seq_lens, K, V, codes, new_lens, ws, stream=None):
     """Of the newest n_new[b] tokens keep rows keep[b][:n_keep[b]] (ascending), moved to the front of them in K, V and
-    codes (or None); new_lens[b] (or None) receives the length that is left."""
+    codes (or None); new_lens[b] (or None; no memory of the inputs) receives the length that is left."""
     _check(_serving.compact_kv(dims, keep, n_keep, n_new, seq_lens, K, V, codes, None, 0, new_lens, ws, _handle(stream), False),
            "hata_compact_kv")
 
 
 def hata_compact_kv_paged(dims: Dims, keep, n_keep, n_new, seq_lens, K_pool, V_pool, codes_pool, block_table,
                           block_size, new_lens, ws, stream=None):
-    """hata_compact_kv over paged pools."""
+    """hata_compact_kv over paged pools.  A sequence that would move rows onto slots that another one holds too (pages shared by a
+    fork and not grown since) is flagged in the status word and left as it is."""
     _check(_serving.compact_kv(dims, keep, n_keep, n_new, seq_lens, K_pool, V_pool, codes_pool, block_table, block_size,
                                new_lens, ws, _handle(stream), True), "hata_compact_kv_paged")
 

@@ -11,8 +11,8 @@
 // decisions are one CTA (a prefix sum over rows and two passes over the counts, kept in shared memory), its copies and
 // compact's moves spread over all SMs as 16-byte vectors.  The kernels are launched early, so a
 // launch overlaps the kernel before it.  Measured on B200: a beam step of 32 sequences over 256-page
-// rows (roll back, fork 8 into 24, grow with 24 copies on write: five kernels) 19-20 us, of which each
-// resize's decisions are about 5; compacting 16 sequences' trees of 64 tokens 3.0 us.
+// rows (roll back, fork 8 into 24, grow with 24 copies on write: five kernels) 19-21 us, of which each
+// resize's decisions are about 5; compacting 16 sequences' trees of 64 tokens 3.0-3.4 us.
 #include <algorithm>
 #include <map>
 #include <mutex>

@@ -13,8 +13,9 @@
 // of 16 bytes, so the mean square is a shuffle tree and the partner of a half-split pair lies rot / 2
 // elements, a whole number of lanes, away.  The 8 warps of a CTA take 8 consecutive tokens and the same rows of
 // each, so that the scattered stores of neighbouring tokens meet in L2 as 2 KB runs per head.
-// Measured on B200: 4 prompts of up to 8192 tokens (32 / 8 heads, bf16, 617 MB in and out on average) 109-116 us, 0.81-0.87 of
-// a copy's bandwidth; one token of 16 sequences into a paged cache 3.0 us.  A warp per four rows of a token, each fetching
+// Measured on B200: 4 prompts of up to 8192 tokens (32 / 8 heads, bf16, 617 MB in and out on average) 108-125 us from one run
+// to another, 0.75-0.87 of a copy's bandwidth; 4 of up to 4096 in fp32 106 us, 0.89; one token of 16 sequences into a paged
+// cache 2.9 us.  A warp per four rows of a token, each fetching
 // positions, table and weights for itself, took 240 us; a warp per token with norm weights, cosines and sines
 // in registers 144 us (two CTAs per SM; with three it spilled, 232 us).
 #include <algorithm>

@@ -8,8 +8,8 @@
 // output.  No barrier inside a run of tiles.  The warps meet once per unit.  Bound by memory: at 6.5 TB/s an SM
 // receives a warp's 8 KB step every 364 cycles, and 128 KB are in flight.  Measured on B200: 16 ragged sequences of
 // 8207 visible slots, 32 / 8 heads, paged, 87-91 us (0.91-0.94 of a copy's bandwidth); 8 x 64K slots 329 us (1.00); 28 rows over
-// 29K slots 31 us (0.58: 3 us of launches, 2 us to find the run, 2 us to meet and 2 us to join are fixed costs); 4 rows
-// over 4.1K slots 9.3 us.
+// 29K slots 30-33 us (0.55-0.59: 3 us of launches, 2 us to find the run, 2 us to meet and 2 us to join are fixed costs); 4 rows
+// over 4.1K slots 9.2-9.4 us; 64 sequences of 4.1K 169 us (0.97).
 //
 // span_simt_kernel (fp32): eight warps, each with 16 slots of a 128-slot tile, on its own: it copies
 // its rows of K and V to shared memory (cp.async), a lane takes one slot and half of the 128 dimensions for the
@@ -691,7 +691,8 @@ constexpr int kSpanMaxRows = 32;
 
 // bf16 with more rows per KV head than a tile of span_mma_kernel holds runs on span_tc_kernel.  Up to two such tiles, both
 // of which read all keys, are faster while the keys are few and the fixed costs count: 64 rows, 8 KV heads (tiles of 128
-// slots in all: us of span_mma_kernel, of span_tc_kernel): 256: 15, 20; 2048: 45, 50; 8192: 181, 111.
+// slots in all: us of span_mma_kernel, of span_tc_kernel): 256: 15, 20; 2048: 45, 50; 8192: 181, 111.  The tiles are counted
+// from max_seq, since the lengths are on the device: a cache that is longer than that and holds little takes the 20.
 constexpr int kSpanTcRows = 32, kSpanTcTiles = 2048;
 bool use_tc(const hata_dims_t& d, int n_tok) {
   const long long rows = (long long)(d.n_q_heads / d.n_kv_heads) * n_tok;

@@ -25,8 +25,8 @@
 // 8 cycles that an SMSP needs for a warp's ex2) and 1060 from P to the next S (768 of MMAs, the rest handing over), while
 // the two streams' MMAs take 2048 of the 3550 that a pair of tiles costs.  Measured on B200: prefill of 8192 positions,
 // window 1024, 4 sinks, 32 / 8 heads 147 us (0.54 of the measured bf16 burst rate over the visible pairs; 164 us, 0.49,
-// when it runs for seconds); 256 rows over 4 x 57K slots 227-235 us (0.61-0.63 of a copy's bandwidth; 260-270 us for seconds on
-// end); 64 rows over 4 x 32K slots 110 us (0.75).
+// when it runs for seconds); 256 rows over 4 x 57K slots 227-236 us (0.61-0.63 of a copy's bandwidth; 286-291 us, 0.50, for
+// seconds on end); 64 rows over 4 x 32K slots 110 us (0.75).
 // Slower than the 154 us that the prefill took then: sixteen row warps with half of the columns each (166 us); half tiles of
 // N = 64, so that scores come while the other half is turned (179 us: twice the handing over, and N = 64 MMAs at two
 // thirds of the rate).
