@@ -9,7 +9,7 @@ links them into hash_aware_top_b200/libhata.so (CUDA runtime linked
 statically), then the benchmark's loop (libhata_e2e.so) and the native half of
 the binding (_serving.<ABI>.so, g++ against the headers of the installed torch).
 Rebuilds only when a source or header is newer than the library; the native
-half also when torch, the interpreter or the compiler's command is another.
+half also when torch, the interpreter or the compiler is another.
 """
 from __future__ import annotations
 
@@ -115,7 +115,7 @@ def build_e2e(cc, flags, verbose=False):
 
 BINDING_SRC = os.path.join(PKG, "binding", "serving.cpp")
 BINDING_LIB = os.path.join(PKG, "_serving" + sysconfig.get_config_var("EXT_SUFFIX"))  # an interpreter finds its own alone
-BINDING_STAMP = os.path.join(BUILD, "serving.json")
+BINDING_STAMP = os.path.join(PKG, "_serving.json")  # what it was built for
 
 
 def binding_built_for() -> str:
@@ -126,35 +126,35 @@ def binding_built_for() -> str:
 
 
 def build_binding(force=False, verbose=False):
-    """The native half of the Python binding.  It calls the C ABI and torch's, so it is rebuilt when a header changes and
-    when the command does: another torch, interpreter or compiler."""
+    """The native half of the Python binding.  It calls the C ABI and torch's, so it is rebuilt when a header changes, and for
+    another torch, interpreter or compiler than the stamp beside it names."""
     import torch  # its headers, its ABI
 
     base = os.path.dirname(torch.__file__)
-    tmp = BINDING_LIB + ".tmp"
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           f'-DHATA_BUILT_FOR="{binding_built_for()}"', "-I", INCLUDE,
-           "-I", os.path.join(base, "include"), "-I", sysconfig.get_paths()["include"],
-           "-I", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
-           BINDING_SRC, "-o", tmp, "-L" + PKG, "-lhata", "-L" + os.path.join(base, "lib"), "-ltorch_python",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    key = [binding_built_for(), base, sys.executable, os.environ.get("CXX", "g++")]
     try:
         with open(BINDING_STAMP) as f:
-            same = json.load(f) == cmd
+            same = json.load(f) == key
     except (OSError, ValueError):
         same = False
     if not force and same and not _stale(BINDING_LIB, [BINDING_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))):
         return
+    tmp = BINDING_LIB + ".tmp"
+    cmd = [key[-1], "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DHATA_BUILT_FOR="{key[0]}"', "-I", INCLUDE,
+           "-I", os.path.join(base, "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
+           BINDING_SRC, "-o", tmp, "-L" + PKG, "-lhata", "-L" + os.path.join(base, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"binding build failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING_LIB)
-    os.makedirs(os.path.dirname(BINDING_STAMP), exist_ok=True)
     with open(BINDING_STAMP, "w") as f:
-        json.dump(cmd, f)
+        json.dump(key, f)
     untagged = os.path.join(PKG, "_serving.so")  # as builds made it before, for any interpreter to find
     if os.path.exists(untagged):
         os.remove(untagged)

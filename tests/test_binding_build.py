@@ -11,7 +11,7 @@ import torch
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
-def test_rebuilt_for_another_torch_or_command(monkeypatch, tmp_path):
+def test_rebuilt_for_another_torch_or_compiler(monkeypatch, tmp_path):
     spec = importlib.util.spec_from_file_location("hata_build_under_test", os.path.join(ROOT, "hash_aware_top_b200", "build.py"))
     B = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(B)
@@ -25,11 +25,13 @@ def test_rebuilt_for_another_torch_or_command(monkeypatch, tmp_path):
 
     monkeypatch.setattr(B, "PKG", str(tmp_path))
     monkeypatch.setattr(B, "BINDING_LIB", str(tmp_path / "_serving.so.here"))
-    monkeypatch.setattr(B, "BINDING_STAMP", str(tmp_path / "stamp" / "serving.json"), raising=False)
+    monkeypatch.setattr(B, "BINDING_STAMP", str(tmp_path / "serving.json"), raising=False)
     monkeypatch.setattr(B, "subprocess", types.SimpleNamespace(run=run))
     B.build_binding()
+    find, B.nvcc = B.nvcc, None  # what is up to date needs no compiler
     B.build_binding()
     assert len(built) == 1
+    B.nvcc = find
     monkeypatch.setattr(torch, "__version__", "1.2.3+other")
     B.build_binding()
     B.build_binding()
