@@ -131,7 +131,7 @@ def build_binding(force=False, verbose=False):
     import torch  # its headers, its ABI
 
     base = os.path.dirname(torch.__file__)
-    key = [binding_built_for(), base, sys.executable, os.environ.get("CXX", "g++")]
+    key = [binding_built_for(), base, sysconfig.get_paths()["include"], os.environ.get("CXX", "g++")]
     try:
         with open(BINDING_STAMP) as f:
             same = json.load(f) == key
